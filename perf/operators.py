@@ -228,7 +228,7 @@ def _plain_plan(st):
 
 
 def _plain_lora_fwd(st):
-    y = st["base"].float()
+    y = st["base"].float().clone()
     for a, idx in st["groups"]:
         u = st["x"][idx].float() @ st["a"][a].float().t()
         y[idx] += st["scale"][a] * (u @ st["b"][a].float().t())
@@ -251,7 +251,7 @@ def _plain_lora_bwd(st):
 def _plain_circ_fwd(st):
     p, T = st["case"]["p"], st["case"]["T"]
     q = st["case"]["D"] // p
-    y = st["base"].float()
+    y = st["base"].float().clone()
     for a, idx in st["groups"]:
         xr, xi = _bins(st["x"][idx].float().view(-1, q, p) @ st["f"], p)
         cr, ci = _bins(st["c_hat"][a], p)
