@@ -31,8 +31,9 @@ LIB = os.path.join(PKG, "librdfft.so")
 EMU = os.path.join(PKG, "librdfft_hostemu.so")
 
 CU_SOURCES = ["rdfft_api.cu", "rdfft_kernels.cu", "rdfft2d_kernels.cu", "convert_kernels.cu", "circ_launch.cu",
-              "circ_tc.cu", "circ_bwd_fused.cu"] + [
-    f"circ_p{p}.cu" for p in (64, 128, 256, 512, 1024, 2048, 4096)]
+              "circ_tc.cu", "circ_bwd_fused.cu", "adapter_plan.cu", "lora_bf16.cu", "lora_f32.cu", "many_launch.cu",
+              "grad_norm.cu"] + [
+    f"circ_{kind}p{p}.cu" for kind in ("", "many_") for p in (64, 128, 256, 512, 1024, 2048, 4096)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,0 +1,148 @@
+// Grouping of a batch's tokens by adapter: a stable counting sort of T keys in [0, n], and
+// the tile lists that the adapter kernels' CTAs read (layout in adapter_plan.h).
+//
+// One CTA of 32 warps; warp w owns a contiguous range of tokens, so counting per warp and
+// then scanning the warps' counts of a bin gives every token a rank that keeps the batch's
+// order, with no atomics and the same result on every run. Lanes with equal keys find each
+// other with a match; the first of them moves the warp's counter. The keys are read twice
+// (4 T bytes, the second time from cache) and 8 T bytes and the lists are written.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "adapter_plan.h"
+#include "internal.h"
+#include "pdl.cuh"
+
+namespace rdfft {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+
+__global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict__ ids, int T, int n, int* plan,
+                                                           PlanLayout lay) {
+  extern __shared__ int sm[];
+  const int bins = n + 1;
+  int* hist = sm;                             // [kWarps][bins]: counts, then next sorted position
+  int* first = sm + kWarps * bins;            // [bins + 1]: offsets
+  int* tile0 = first + bins + 1;              // [kPlanLists][bins + 1]: first tile of each group
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int i = threadIdx.x; i < kWarps * bins; i += kThreads) hist[i] = 0;
+  griddep_wait();                             // ids are complete, readers of the old plan are done
+  __syncthreads();
+
+  const int per = (T + kThreads - 1) / kThreads * 32;                 // tokens per warp, whole steps
+  const int64_t beg64 = (int64_t)w * per;
+  const int beg = beg64 < T ? (int)beg64 : T, end = T - beg < per ? T : beg + per;
+  int* mine = hist + w * bins;
+  auto key_at = [&](int t) {                  // an id outside [0, n) is "no adapter": bin n
+    const int id = t < end ? __ldg(ids + t) : -1;
+    return (unsigned)id < (unsigned)n ? id : n;
+  };
+  // kAhead steps' keys are requested together, so a step does not wait for memory
+  constexpr int kAhead = 8;
+  for (int t0 = beg; t0 < end; t0 += 32 * kAhead) {
+    int key[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) key[s] = key_at(t0 + 32 * s + lane);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int t = t0 + 32 * s + lane;
+      const unsigned in = __ballot_sync(~0u, t < end);
+      if (in == 0) break;
+      const unsigned same = __match_any_sync(~0u, key[s]) & in;
+      if (t < end && lane == __ffs(same) - 1) mine[key[s]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+
+  // per bin: the warps' counts become ranks within the group
+  for (int b = threadIdx.x; b < bins; b += kThreads) {
+    int sum = 0;
+#pragma unroll 8
+    for (int i = 0; i < kWarps; ++i) {
+      const int c = hist[i * bins + b];
+      hist[i * bins + b] = sum;
+      sum += c;
+    }
+    first[b] = sum;
+#pragma unroll
+    for (int l = 0; l < kPlanLists; ++l) tile0[l * (bins + 1) + b] = (sum + plan_tile(l) - 1) / plan_tile(l);
+  }
+  __syncthreads();
+  // exclusive scans of the counts (warp 0) and of each list's tiles (warps 1 to 3)
+  if (w <= kPlanLists) {
+    int* v = w == 0 ? first : tile0 + (w - 1) * (bins + 1);
+    int carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += 32) {
+      const int b = b0 + lane;
+      const int x = b < bins ? v[b] : 0;
+      int s = x;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(~0u, s, d);
+        if (lane >= d) s += o;
+      }
+      if (b < bins) v[b] = carry + s - x;
+      carry += __shfl_sync(~0u, s, 31);
+    }
+    if (lane == 0) {
+      v[bins] = carry;
+      if (w > 0) plan[1 + w] = carry;
+    }
+  }
+  if (threadIdx.x == 0) {
+    plan[0] = T;
+    plan[1] = n;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b <= bins; b += kThreads) plan[lay.offsets + b] = first[b];
+
+  // the ranks place the tokens; the first token of every tile writes the tile
+  for (int t0 = beg; t0 < end; t0 += 32 * kAhead) {
+    int key[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) key[s] = key_at(t0 + 32 * s + lane);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int t = t0 + 32 * s + lane;
+      const unsigned in = __ballot_sync(~0u, t < end);
+      if (in == 0) break;
+      const unsigned same = __match_any_sync(~0u, key[s]) & in;
+      int base = 0;
+      if (t < end) base = mine[key[s]];
+      __syncwarp();
+      if (t < end) {
+        const int rank = base + __popc(same & ((1u << lane) - 1));
+        const int pos = first[key[s]] + rank;
+        plan[lay.order + pos] = t;
+        plan[lay.group + pos] = key[s];
+#pragma unroll
+        for (int l = 0; l < kPlanLists; ++l)
+          if (rank % plan_tile(l) == 0) {
+            const int64_t tile = tile0[l * (bins + 1) + key[s]] + rank / plan_tile(l);
+            *reinterpret_cast<int2*>(plan + lay.tiles[l] + 2 * tile) = make_int2(pos, key[s]);
+          }
+        if (lane == __ffs(same) - 1) mine[key[s]] = base + __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_plan(const int* ids, int64_t T, int n, int* plan, cudaStream_t s) {
+  const int bins = n + 1;
+  const size_t smem = sizeof(int) * ((size_t)kWarps * bins + (size_t)(kPlanLists + 1) * (bins + 1));
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_adapter_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k_adapter_plan, dim3(1), dim3(kThreads), smem, s, ids, (int)T, n, plan, plan_layout(T, n));
+}
+
+}  // namespace rdfft

@@ -31,6 +31,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "layer_policy.h"
 #include "packed_fft.cuh"
@@ -100,8 +102,10 @@ __device__ __forceinline__ void fft_rows(float* tile, int NR, SrcFn src) {
 
 // Last pass of a forward transform over tile rows [0, NR), written to global rows
 // dst(r) (nullptr: dropped) with the mirror epilogue: the Hartley form of the inverse.
-template <int P, int NT, typename T, typename DstFn>
-__device__ __forceinline__ void last_pass_mirror_to_global(float* tile, int NR, DstFn dst) {
+// BaseFn, when given (not NoBase), names the row that is added to row r as it is stored.
+struct NoBase {};
+template <int P, int NT, typename T, typename DstFn, typename BaseFn = NoBase>
+__device__ __forceinline__ void last_pass_mirror_to_global(float* tile, int NR, DstFn dst, BaseFn base = BaseFn()) {
   using G = LayerGeo<P>;
   constexpr int K = G::NPASS - 1;
   constexpr int TPR = G::TPR, RPR = NT / TPR;
@@ -109,23 +113,29 @@ __device__ __forceinline__ void last_pass_mirror_to_global(float* tile, int NR, 
   const int v = threadIdx.x % TPR;
   for (int r = threadIdx.x / TPR; r < NR; r += RPR) {
     T* g = dst(r);
-    generic_pass<G, K, false, 0, 1, T, 1>(tile, r, v, g, g != nullptr);
+    if constexpr (std::is_same_v<BaseFn, NoBase>)
+      generic_pass<G, K, false, 0, 1, T, 1>(tile, r, v, g, g != nullptr);
+    else
+      generic_pass<G, K, false, 0, 2, T, 1>(tile, r, v, g, g != nullptr, base(r));
   }
   for (int r = threadIdx.x; r < NR; r += NT) {
     T* g = dst(r);
-    merged_orbit<G, K, false, 0, 1, T, 1>(tile, r, 0, g, g != nullptr);
+    if constexpr (std::is_same_v<BaseFn, NoBase>)
+      merged_orbit<G, K, false, 0, 1, T, 1>(tile, r, 0, g, g != nullptr);
+    else
+      merged_orbit<G, K, false, 0, 2, T, 1>(tile, r, 0, g, g != nullptr, base(r));
   }
 }
 
-template <int P, int NT, typename T, int K, typename DstFn>
-__device__ __forceinline__ void fwd_tile_passes_then_mirror(float* tile, int NR, DstFn dst) {
+template <int P, int NT, typename T, int K, typename DstFn, typename BaseFn = NoBase>
+__device__ __forceinline__ void fwd_tile_passes_then_mirror(float* tile, int NR, DstFn dst, BaseFn base = BaseFn()) {
   using G = LayerGeo<P>;
   __syncthreads();
   if constexpr (K < G::NPASS - 1) {
     tile_orbit_pass<P, NT, K, false, T>(tile, NR);
-    fwd_tile_passes_then_mirror<P, NT, T, K + 1>(tile, NR, dst);
+    fwd_tile_passes_then_mirror<P, NT, T, K + 1>(tile, NR, dst, base);
   } else {
-    last_pass_mirror_to_global<P, NT, T>(tile, NR, dst);
+    last_pass_mirror_to_global<P, NT, T>(tile, NR, dst, base);
   }
 }
 
@@ -135,8 +145,8 @@ __device__ __forceinline__ void fwd_tile_passes_then_mirror(float* tile, int NR,
 // of the tile rows with the mirror and the 1/p applied as the last pass writes row r
 // to dst(r). The forward butterflies cost 6 FP instructions per group against the
 // inverse's 8.
-template <int P, int NT, typename T, typename DstFn>
-__device__ __forceinline__ void ifft_rows_mirrored(float* tile, int NR, DstFn dst) {
+template <int P, int NT, typename T, typename DstFn, typename BaseFn = NoBase>
+__device__ __forceinline__ void ifft_rows_mirrored(float* tile, int NR, DstFn dst, BaseFn base = BaseFn()) {
   using G = LayerGeo<P>;
   constexpr int TPR = G::TPR, RPR = NT / TPR;
   const int v = threadIdx.x % TPR;
@@ -148,7 +158,7 @@ __device__ __forceinline__ void ifft_rows_mirrored(float* tile, int NR, DstFn ds
     __syncthreads();
     if (r < NR) fwd_pass0_finish<G>(a, v, tile + G::row_base(r));
   }
-  fwd_tile_passes_then_mirror<P, NT, T, 1>(tile, NR, dst);
+  fwd_tile_passes_then_mirror<P, NT, T, 1>(tile, NR, dst, base);
 }
 
 // Packed-bin view of a row: bin 0 is the real pair (slot 0, slot p/2); bin k > 0 is
@@ -160,22 +170,26 @@ __device__ __forceinline__ int bin_im_slot(int k) { return k == 0 ? P / 2 : P - 
 // BWDX = false: in = x, out = y; the CTA's QI output blocks are i, summed over j.
 // BWDX = true : in = g, out = grad_x; the CTA's QI output blocks are j, summed over i,
 //               against conj(c_hat).
-template <int P, typename T, int NT, int TT, int NS, bool BWDX>
-// 256-thread CTAs are declared for two per SM (<= 128 registers), 512-thread ones for one
-__global__ void __launch_bounds__(NT, NT >= 512 ? 1 : (NT >= 256 ? 2 : 1))
-k_circ_x(const T* __restrict__ in, const float* __restrict__ chat, T* __restrict__ out,
-         int64_t B, int q, int QI) {
+// The tokens of a CTA: token t of it is row row(t) of the activations, ntok of them (<= TT).
+// Here consecutive rows; circ_many.cuh takes them from a plan.
+struct DenseTokens {
+  int64_t tok0;
+  int ntok;
+  __device__ __forceinline__ int64_t row(int t) const { return tok0 + t; }
+};
+
+template <int P, typename T, int NT, int TT, int NS, bool BWDX, typename Tokens, typename BaseFn = NoBase>
+__device__ __forceinline__ void circ_x_body(const T* __restrict__ in, const float* __restrict__ chat,
+                                            T* __restrict__ out, const Tokens& tok, int q, int QI, int o0,
+                                            BaseFn base = BaseFn()) {
   extern __shared__ float tile[];
   const int D = q * P;
-  const int64_t tok0 = (int64_t)blockIdx.x * TT;
-  const int ntok = (int)((B - tok0) < TT ? (B - tok0) : TT);
-  const int o0 = blockIdx.y * QI;            // first output block of this CTA
-  griddep_wait();                            // earlier work in the stream (c_hat, the input) is done
+  const int ntok = tok.ntok;
 
   // 1. rdFFT of the TT*q input rows (row r = t*q + b)
   fft_rows<P, NT, T>(tile, TT * q, [&](int r) -> const T* {
     const int t = r / q, b = r - t * q;
-    return t < ntok ? in + (tok0 + t) * (int64_t)D + (int64_t)b * P : nullptr;
+    return t < ntok ? in + tok.row(t) * (int64_t)D + (int64_t)b * P : nullptr;
   });
   __syncthreads();
 
@@ -404,32 +418,39 @@ k_circ_x(const T* __restrict__ in, const float* __restrict__ chat, T* __restrict
   griddep_launch_dependents();
   ifft_rows_mirrored<P, NT, T>(tile, TT * QI, [&](int r) -> T* {
     const int t = r / QI, ol = r - t * QI;
-    return t < ntok ? out + (tok0 + t) * (int64_t)D + (int64_t)(o0 + ol) * P : nullptr;
-  });
+    return t < ntok ? out + tok.row(t) * (int64_t)D + (int64_t)(o0 + ol) * P : nullptr;
+  }, base);
+}
+
+template <int P, typename T, int NT, int TT, int NS, bool BWDX>
+// 256-thread CTAs are declared for two per SM (<= 128 registers), 512-thread ones for one
+__global__ void __launch_bounds__(NT, NT >= 512 ? 1 : (NT >= 256 ? 2 : 1))
+k_circ_x(const T* __restrict__ in, const float* __restrict__ chat, T* __restrict__ out,
+         int64_t B, int q, int QI) {
+  DenseTokens tok;
+  tok.tok0 = (int64_t)blockIdx.x * TT;
+  tok.ntok = (int)((B - tok.tok0) < TT ? (B - tok.tok0) : TT);
+  griddep_wait();                            // earlier work in the stream (c_hat, the input) is done
+  circ_x_body<P, T, NT, TT, NS, BWDX>(in, chat, out, tok, q, QI, blockIdx.y * QI);
 }
 
 // ---------------------------------------------------------------------- grad_c
 // Thread group gamma = (k, ib, jb): bin k, output blocks i = ib*RI .. +RI, input
 // blocks jl = jb*RJ .. +RJ of the CTA's QJ-block group. The tile holds, per tile of
 // ntok <= TT tokens, G for rows t*q + i and X for rows ntok*q + t*QJ + jl.
-template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
-__global__ void __launch_bounds__(NT, 1)
-k_circ_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ grad_c,
-          float* __restrict__ partial, int64_t B, int q, int QJ, int64_t tok_per_cta, int ifft_here) {
+// The body sums the tokens at positions [tbeg, tend) of `tok`. Its sums are stored into
+// gc_base when `store` (else added to it), or inverse-transformed straight into gc_base when
+// ifft_here (the caller guarantees that the tile holds the CTA's q QJ rows).
+template <int P, typename T, int NT, int TT, int NG, int RI, int RJ, typename Tokens>
+__device__ __forceinline__ void circ_gc_body(const T* __restrict__ g, const T* __restrict__ x,
+                                             float* __restrict__ gc_base, const Tokens& tok, int64_t tbeg,
+                                             int64_t tend, int q, int QJ, bool store, int ifft_here) {
   extern __shared__ float tile[];
   constexpr int HB = P / 2;
   const int D = q * P;
   const int j0 = blockIdx.y * QJ;
-  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
-  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
   const int nib = q / RI, njb = QJ / RJ;
   const int ngroups = HB * nib * njb;
-  // the only token slice: this CTA's sums are final and every (bin, i, j) of its group
-  // is one thread-group's, so it stores them instead of adding into a zeroed grad_c; with
-  // per-slice sums (partial), each slice stores its own q x q x p spectrum the same way
-  const bool store = (gridDim.x == 1) || partial != nullptr;
-  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * q * q * P : grad_c;
-  griddep_wait();                            // earlier work in the stream (g, x, zeroed grad_c) is done
 
   if constexpr (RJ % 2 == 0) {
     // S accumulators: input blocks b and b + 1 of a group on packed fp32 pairs (RJ even),
@@ -452,11 +473,11 @@ k_circ_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ 
       fft_rows<P, NT, T>(tile, ntok * (q + QJ), [&](int r) -> const T* {
         if (r < xrow0) {
           const int t = r / q, b = r - t * q;
-          return g + (tok0 + t) * (int64_t)D + (int64_t)b * P;
+          return g + tok.row(tok0 + t) * (int64_t)D + (int64_t)b * P;
         }
         const int rr = r - xrow0;
         const int t = rr / QJ, jl = rr - t * QJ;
-        return x + (tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
+        return x + tok.row(tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
       });
       __syncthreads();
       // bin0 = false (warps with no bin-0 group) drops the real-pair selects
@@ -561,11 +582,11 @@ k_circ_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ 
       fft_rows<P, NT, T>(tile, ntok * (q + QJ), [&](int r) -> const T* {
         if (r < xrow0) {
           const int t = r / q, b = r - t * q;
-          return g + (tok0 + t) * (int64_t)D + (int64_t)b * P;
+          return g + tok.row(tok0 + t) * (int64_t)D + (int64_t)b * P;
         }
         const int rr = r - xrow0;
         const int t = rr / QJ, jl = rr - t * QJ;
-        return x + (tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
+        return x + tok.row(tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
       });
       __syncthreads();
   #pragma unroll
@@ -642,9 +663,28 @@ k_circ_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ 
     // form, the rows stored mirrored above) straight to grad_c, in place of a separate launch
     __syncthreads();
     ifft_rows_mirrored<P, NT, float>(tile, q * QJ, [&](int r) -> float* {
-      return grad_c + ((int64_t)(r / QJ) * q + j0 + r % QJ) * P;
+      return gc_base + ((int64_t)(r / QJ) * q + j0 + r % QJ) * P;
     });
   }
+}
+
+struct DensePositions {
+  __device__ __forceinline__ int64_t row(int64_t pos) const { return pos; }
+};
+
+template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ grad_c,
+          float* __restrict__ partial, int64_t B, int q, int QJ, int64_t tok_per_cta, int ifft_here) {
+  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
+  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
+  // the only token slice: this CTA's sums are final and every (bin, i, j) of its group
+  // is one thread-group's, so it stores them instead of adding into a zeroed grad_c; with
+  // per-slice sums (partial), each slice stores its own q x q x p spectrum the same way
+  const bool store = (gridDim.x == 1) || partial != nullptr;
+  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * q * q * P : grad_c;
+  griddep_wait();                            // earlier work in the stream (g, x, zeroed grad_c) is done
+  circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, gc_base, DensePositions(), tbeg, tend, q, QJ, store, ifft_here);
 }
 
 // ------------------------------------------------------------------ launchers

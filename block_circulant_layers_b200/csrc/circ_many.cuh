@@ -1,0 +1,193 @@
+// Block-circulant adapters of many requests: the layer kernels of circ_kernels.cuh over a
+// batch whose tokens each use one of n adapters, or none (a plan, adapter_plan.h).
+//
+//     forward : y_t = base_t + W(c_a) x_t      grad_x_t = W(c_a)^T g_t     a = adapter of t
+//     grad_c  : grad_c[a] = the packed cross-spectrum summed over the tokens of a, inverted
+//
+// A CTA takes up to TT tokens of one adapter (a tile of the plan, or part of one) and runs the
+// dense layer's body on them, reading its rows through the plan's order and its adapter's part
+// of c_hat, so a c_hat read from L2 serves the same number of tokens as in the dense layer.
+// The base row is added in fp32 as the last transform pass stores a row.
+#pragma once
+
+#include "circ_kernels.cuh"
+#include "lora.cuh"
+#include "many_policy.h"
+
+namespace rdfft {
+
+struct PlannedTokens {
+  const int* order;
+  int ntok;
+  __device__ __forceinline__ int64_t row(int t) const { return __ldg(order + t); }
+};
+struct PlannedPositions {
+  const int* order;
+  __device__ __forceinline__ int64_t row(int64_t pos) const { return __ldg(order + pos); }
+};
+
+template <int P, typename T, int NT, int TT, int NS, bool BWDX>
+__global__ void __launch_bounds__(NT, NT >= 512 ? 1 : (NT >= 256 ? 2 : 1))
+k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T* base, T* out, int q, int QI,
+              PlanView plan, const int* __restrict__ group) {
+  griddep_wait();
+  if (!plan_matches(plan)) return;
+  int pos, ad, m;
+  if constexpr (TT == 1) {
+    pos = blockIdx.x;                                       // one token per CTA: no tile list
+    ad = __ldg(group + pos);
+    m = 1;
+  } else {
+    static_assert(TT == 2 || TT == 4, "a CTA takes a whole tile of the 4-token list, or half of it");
+    const int sub = blockIdx.x % (4 / TT), tile = blockIdx.x / (4 / TT);
+    const int2 te = __ldg(plan.tiles + tile);               // within the list's capacity
+    if (tile >= __ldg(plan.header + 2 + plan.list)) return;
+    pos = te.x + sub * TT, ad = te.y;
+    m = min(__ldg(plan.offsets + ad + 1) - pos, TT);
+    if (m <= 0) return;
+  }
+  const int o0 = blockIdx.y * QI, D = q * P;
+  PlannedTokens tok{plan.order + pos, m};
+  if (ad >= plan.n) {                                       // no adapter: the base row, or zeros
+    if (base == out) return;
+    for (int e = threadIdx.x; e < m * QI * P; e += NT) {
+      const int64_t at = tok.row(e / (QI * P)) * D + o0 * P + e % (QI * P);
+      out[at] = base ? base[at] : from_f32<T>(0.0f);
+    }
+    return;
+  }
+  const float* c = chat + (int64_t)ad * q * q * P;
+  circ_x_body<P, T, NT, TT, NS, BWDX>(in, c, out, tok, q, QI, o0, [&](int r) -> const T* {
+    const int t = r / QI, ol = r - t * QI;
+    return (base != nullptr && t < m) ? base + tok.row(t) * (int64_t)D + (int64_t)(o0 + ol) * P : nullptr;
+  });
+}
+
+// grid: token slices x input-block groups x adapters. Slice s of adapter a sums an equal part
+// of the adapter's tokens (whole tiles) into its own q x q x p spectrum.
+template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_many_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ sums, int q, int QJ,
+               PlanView plan, int ifft_here) {
+  griddep_wait();
+  if (!plan_matches(plan)) return;
+  const int ad = blockIdx.z;
+  const int64_t beg = __ldg(plan.offsets + ad), end = __ldg(plan.offsets + ad + 1);
+  const int64_t tiles = (end - beg + TT - 1) / TT, per = (tiles + gridDim.x - 1) / gridDim.x * TT;
+  const int64_t tbeg = min(beg + (int64_t)blockIdx.x * per, end), tend = min(tbeg + per, end);
+  float* const gc = sums + ((int64_t)blockIdx.x * plan.n + ad) * q * q * P;
+  circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, gc, PlannedPositions{plan.order}, tbeg, tend, q, QJ, true, ifft_here);
+}
+
+template <int P, typename T, int NT, int TT, int NS, bool BWDX>
+static cudaError_t launch_many_x_cfg(const CircMany& a, cudaStream_t s) {
+  constexpr int QI_MAX = NS * NT / (P / 2);
+  const int q = a.D / P;
+  const PlanLayout lay = plan_layout(a.T, a.n);
+  const int64_t gx = TT == 1 ? a.T : lay.cap[0] * (4 / TT);
+  if (gx > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int QI = layer_qi(q, QI_MAX, gx, num_sms());
+  const size_t smem = sizeof(float) * (size_t)LayerGeo<P>::words(TT * q);
+  auto kern = k_circ_many_x<P, T, NT, TT, NS, BWDX>;
+  const cudaError_t e = set_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)gx, (unsigned)(q / QI)), dim3(NT), smem, s, static_cast<const T*>(a.in),
+                    a.c_hat, static_cast<const T*>(a.base), static_cast<T*>(a.out), q, QI,
+                    plan_view(a.plan, a.T, a.n, 0), a.plan + lay.group);
+}
+
+// The dense layer's shapes (launch_x_p), with the tokens per CTA bounded by the mean group.
+template <int P, typename T, bool BWDX>
+static cudaError_t launch_many_x_p(const CircMany& a, cudaStream_t s) {
+  const int q = a.D / P;
+  if constexpr (P <= 512) {
+    constexpr int NT = 256;
+    constexpr int NS = (8 * (P / 2)) / NT > 0 ? (8 * (P / 2)) / NT : 1;
+    const int tt = circ_many_tokens(a.T, a.n, q, NS * NT / (P / 2), num_sms(), NS * 4 <= 32 ? 4 : 2);
+    if constexpr (P == 128) {
+      if (tt > 1 && a.T >= 256 && q >= 16) return launch_many_x_cfg<P, T, 512, 2, 4, BWDX>(a, s);
+    }
+    if constexpr (NS * 4 <= 32) {
+      if (tt == 4) return launch_many_x_cfg<P, T, NT, 4, NS, BWDX>(a, s);
+    }
+    if (tt == 2) return launch_many_x_cfg<P, T, NT, 2, NS, BWDX>(a, s);
+    return launch_many_x_cfg<P, T, NT, 1, NS, BWDX>(a, s);
+  } else {
+    constexpr int NT = 128;
+    constexpr int NS1 = (P / 2) / NT;
+    constexpr int NSM = P == 2048 ? 16 : (NS1 * 4 <= 32 ? NS1 * 4 : 32);
+    if constexpr (P > 1024) {
+      if (q == 1) return launch_many_x_cfg<P, T, NT, 1, NS1, BWDX>(a, s);
+    }
+    return launch_many_x_cfg<P, T, NT, 1, NSM, BWDX>(a, s);
+  }
+}
+
+template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
+static cudaError_t run_many_gc(const CircMany& a, int QJ, cudaStream_t s, GcSink* sink) {
+  const int q = a.D / P;
+  auto kern = k_circ_many_gc<P, T, NT, TT, NG, RI, RJ>;
+  const size_t smem = sizeof(float) * (size_t)LayerGeo<P>::words(TT * (q + QJ));
+  const int njgroups = q / QJ;
+  const int slices = circ_many_slices(a.T, a.n, njgroups, TT, num_sms());
+  const bool here = slices == 1 && (int64_t)q * QJ <= (int64_t)TT * (q + QJ);
+  float* partial = nullptr;
+  cudaError_t e = sink_plan(sink, slices, (int64_t)a.n * q * q * P, &partial);
+  sink->ifft_done = here;
+  if (e != cudaSuccess || sink->plan_only) return e;
+  if (slices > 1 && partial == nullptr) return cudaErrorInvalidValue;
+  e = set_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)slices, (unsigned)njgroups, (unsigned)a.n), dim3(NT), smem, s,
+                    static_cast<const T*>(a.g), static_cast<const T*>(a.in), partial ? partial : a.grad_c, q, QJ,
+                    plan_view(a.plan, a.T, a.n, 0), here ? 1 : 0);
+}
+
+// Accumulator shapes as launch_gc_tt.
+template <int P, typename T>
+static cudaError_t launch_many_gc_p(const CircMany& a, cudaStream_t s, GcSink* sink) {
+  constexpr int TT = (P >= 2048) ? 1 : (P >= 1024 ? 2 : 4);
+  constexpr int NT = 512;
+  constexpr int HB = P / 2;
+  const int q = a.D / P;
+  const int QJ = layer_qj(q, HB, 32LL * NT, (a.T + TT - 1) / TT, num_sms());
+  if ((int64_t)HB * q * QJ > 32LL * NT) return cudaErrorInvalidConfiguration;
+  const int64_t slots = (int64_t)HB * q * QJ;
+  if (q % 4 == 0 && QJ % 8 == 0) return run_many_gc<P, T, NT, TT, 1, 4, 8>(a, QJ, s, sink);
+  if (q % 4 == 0 && QJ % 4 == 0) {
+    if (slots <= 16LL * NT) return run_many_gc<P, T, NT, TT, 1, 4, 4>(a, QJ, s, sink);
+    return run_many_gc<P, T, NT, TT, 2, 4, 4>(a, QJ, s, sink);
+  }
+  if (q % 2 == 0 && QJ % 2 == 0) {
+    if (slots <= 4LL * NT) return run_many_gc<P, T, NT, TT, 1, 2, 2>(a, QJ, s, sink);
+    if (slots <= 8LL * NT) return run_many_gc<P, T, NT, TT, 2, 2, 2>(a, QJ, s, sink);
+    if (slots <= 16LL * NT) return run_many_gc<P, T, NT, TT, 4, 2, 2>(a, QJ, s, sink);
+    return run_many_gc<P, T, NT, TT, 8, 2, 2>(a, QJ, s, sink);
+  }
+  if (slots <= 1LL * NT) return run_many_gc<P, T, NT, TT, 1, 1, 1>(a, QJ, s, sink);
+  if (slots <= 4LL * NT) return run_many_gc<P, T, NT, TT, 4, 1, 1>(a, QJ, s, sink);
+  if (slots <= 8LL * NT) return run_many_gc<P, T, NT, TT, 8, 1, 1>(a, QJ, s, sink);
+  if (slots <= 16LL * NT) return run_many_gc<P, T, NT, TT, 16, 1, 1>(a, QJ, s, sink);
+  return run_many_gc<P, T, NT, TT, 32, 1, 1>(a, QJ, s, sink);
+}
+
+// op 0 = forward (in = x), 1 = grad_x (in = g), 2 = grad_c (g, in = x; see circ_layer_p).
+template <int P>
+cudaError_t circ_many_p(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink) {
+  if (dtype == 0) {
+    if (op == 0) return launch_many_x_p<P, float, false>(a, s);
+    if (op == 1) return launch_many_x_p<P, float, true>(a, s);
+    return launch_many_gc_p<P, float>(a, s, sink);
+  }
+  if (op == 0) return launch_many_x_p<P, bf16_t, false>(a, s);
+  if (op == 1) return launch_many_x_p<P, bf16_t, true>(a, s);
+  return launch_many_gc_p<P, bf16_t>(a, s, sink);
+}
+
+#define RDFFT_CIRC_MANY_INSTANCE(PP)                                                                      \
+  cudaError_t circ_many_##PP(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink) {        \
+    return circ_many_p<PP>(op, a, dtype, s, sink);                                                        \
+  }                                                                                                       \
+  cudaError_t take_circ_many_error_##PP(unsigned int* flags) { return take_error_word(flags); }
+
+}  // namespace rdfft

@@ -47,6 +47,10 @@ struct GcSink {
   bool ifft_done = false;        // out: the kernel also ran grad_c's rdIFFT (one slice)
 };
 
+// After a grad_c launch: the ordered sum of the slices, if the sink holds several, then the
+// in-place rdIFFT of grad_c's rows unless the kernel ran it itself.
+cudaError_t finish_grad_c(const GcSink& sink, float* grad_c, int64_t rows, int p, cudaStream_t s);
+
 // Backward in one kernel (grad_x and the grad_c cross-spectrum from one transform of g
 // and x per input-block group) for the shapes it covers (circ_bwd_fused_supported: D = 4096
 // at p = 128, 512 or 1024, and layers of one or two blocks, D in {p, 2p},
@@ -72,5 +76,46 @@ cudaError_t launch_circ_bwd(const void* g, const void* x, const float* c_hat, vo
 // Token slices of the grad_c launch that launch_circ_bwd would make for these sizes with
 // grad_c requested (and grad_x too if with_grad_x); enqueues nothing.
 cudaError_t plan_circ_bwd(int64_t B, int D, int p, int dtype, bool with_grad_x, int* slices);
+
+// ---- adapters of many requests (see adapter_plan, lora_* and circ_*_many in rdfft.h)
+
+// Groups the T tokens of `ids` by adapter into `plan` (adapter_plan.h).
+cudaError_t launch_adapter_plan(const int* ids, int64_t T, int n, int* plan, cudaStream_t s);
+
+// One call of the many-adapter block-circulant layer. Forward: in = x. grad_x: in = g.
+// grad_c: in = x and g.
+struct CircMany {
+  const void* in = nullptr;
+  const void* g = nullptr;
+  const float* c_hat = nullptr;
+  const void* base = nullptr;
+  void* out = nullptr;
+  float* grad_c = nullptr;
+  const int* plan = nullptr;
+  int64_t T = 0;
+  int D = 0, n = 0;
+};
+// op 0 = forward, 1 = grad_x, 2 = grad_c (the sink as in launch_circ_bwd; with several slices
+// its partial buffer is required, and plan_only fills in the slice count).
+cudaError_t launch_circ_many(int op, const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink);
+
+// Low-rank adapters: rows (forward: in = x, w1 = a, w2 = b; bwd: in = g, w1 = b, w2 = a) and
+// weight gradients. Arguments as lora_fwd / lora_bwd in rdfft.h.
+cudaError_t launch_lora_rows(bool bwd, const void* in, const void* w1, const void* w2, const float* scale,
+                             const void* base, void* out, float* mid, const int* plan, int64_t T, int K, int N,
+                             int r, int n, int dtype, cudaStream_t s);
+cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, const float* v, const float* scale,
+                              float* grad_a, float* grad_b, const int* plan, int64_t T, int K, int N, int r, int n,
+                              int dtype, cudaStream_t s);
+
+// Reads and clears the error words of the kernels that take a plan (bit 0: a plan of other
+// sizes was given).
+cudaError_t take_plan_device_error(unsigned int* flags);
+
+// Global norm and clipping of many tensors (grad_norm, clip_grad_norm in rdfft.h). `ws` holds
+// grad_norm_ws_doubles(count) doubles; out == nullptr computes the norm alone.
+int64_t grad_norm_ws_doubles(int count);
+cudaError_t launch_grad_norm(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes,
+                             int count, float max_norm, float* norm, double* ws, cudaStream_t s);
 
 }  // namespace rdfft

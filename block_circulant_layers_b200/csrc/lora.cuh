@@ -1,0 +1,132 @@
+// Shared pieces of the low-rank adapter kernels (lora_bf16.cu, lora_f32.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "adapter_plan.h"
+#include "internal.h"
+#include "packed_fft.cuh"
+#include "pdl.cuh"
+
+namespace rdfft {
+
+// The parts of a plan that one kernel reads, and the sizes it must have been made for.
+struct PlanView {
+  const int* header;
+  const int* offsets;
+  const int* order;
+  const int2* tiles;
+  int list;
+  int T, n;
+};
+
+inline PlanView plan_view(const int* plan, int64_t T, int n, int list) {
+  const PlanLayout l = plan_layout(T, n);
+  PlanView v;
+  v.header = plan;
+  v.offsets = plan + l.offsets;
+  v.order = plan + l.order;
+  v.tiles = reinterpret_cast<const int2*>(plan + l.tiles[list]);
+  v.list = list;
+  v.T = (int)T;
+  v.n = n;
+  return v;
+}
+
+// Set by a kernel that was given a plan of other sizes; that kernel then writes nothing.
+// One word per translation unit, read and cleared by rdfft_take_device_error.
+static __device__ unsigned int g_plan_error;
+
+// Uniform over the grid.
+__device__ __forceinline__ bool plan_matches(const PlanView& v) {
+  if (__ldg(v.header) == v.T && __ldg(v.header + 1) == v.n) return true;
+  if (threadIdx.x == 0) atomicOr(&g_plan_error, 1u);
+  return false;
+}
+
+static cudaError_t take_error_word(unsigned int* flags) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, g_plan_error, sizeof(*flags));
+  if (e != cudaSuccess || *flags == 0) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_plan_error, &zero, sizeof(zero));
+}
+
+// One direction of a low-rank adapter: rows of `in` (T x K) through w1 and w2 to rows of
+// `out` (T x N):  mid_t = w1 in_t (r values), out_t = base_t + scale w2 mid_t.
+// Forward: w1 = A (r x K), w2 = B (N x r). Backward for the input: in = g, w1 = B^T,
+// w2 = A^T, both read where A and B lie (the kernels' BWD), and no base.
+template <typename T>
+struct LoraRows {
+  const T* in;
+  const T* w1;
+  const T* w2;
+  const float* scale;      // n, or nullptr for 1
+  const T* base;           // T x N or nullptr; may be `out`
+  T* out;                  // T x N, or nullptr to compute mid alone
+  float* mid;              // T x r or nullptr: forward u = A x, backward v = scale B^T g
+  int K, N, r;
+  PlanView plan;
+};
+
+// Weight gradients over the tokens of each adapter:
+//   grad_a[a] (r x K) = sum_t v_t x_t^T,  grad_b[a] (N x r) = scale_a sum_t g_t u_t^T.
+template <typename T>
+struct LoraWgrad {
+  const T* x;
+  const T* g;
+  const float* u;
+  const float* v;
+  const float* scale;
+  float* grad_a;
+  float* grad_b;
+  int K, N, r;
+  PlanView plan;
+};
+
+// Cluster of this CTA (one-dimensional).
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned v;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned v;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t map_rank(const void* p, unsigned rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// launch_pdl with the grid cut into clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_cluster_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                                      cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+}  // namespace rdfft

@@ -566,7 +566,8 @@ RD_HD void mirror_pair(float& lo, float& hi, float scale) {
 }
 
 // Generic slots CI.. of a middle/last pass K >= 1 for thread v of the tile row at
-// `trow` (global row g). SRC/DST: 0 = tile, 1 = global row (natural order). Each
+// `trow` (global row g). SRC/DST: 0 = tile, 1 = global row (natural order), DST 2 = global
+// row plus the row at `gb` (fp32 sum, rounded once; gb may be g or null). Each
 // generic orbit is gathered, transformed and written back to the same positions, so
 // a pass needs no synchronisation inside itself. A slot whose residue is 0 (the
 // merged orbit) is skipped here: the merged orbits of all rows are done by
@@ -578,7 +579,7 @@ RD_HD void mirror_pair(float& lo, float& hi, float scale) {
 // [c + (c>>S)] and the one at R0 + c - r (1 <= r) at [R0 + (R0>>S) - r - ((r-1)>>S)] +
 // [c + ((c-1)>>S)]: a per-thread base plus an immediate.
 template <class G, int K, bool INV, int SRC, int DST, int EPI, int CI, typename T, int E>
-RD_HD void generic_slots(float (&a)[E], float* trow, int v, T* g, bool active) {
+RD_HD void generic_slots(float (&a)[E], float* trow, int v, T* g, bool active, const T* gb = nullptr) {
   using S = PassShape<G, K>;
   constexpr int SH = G::S;
   if constexpr (CI < S::C) {
@@ -600,7 +601,7 @@ RD_HD void generic_slots(float (&a)[E], float* trow, int v, T* g, bool active) {
       }
       orbit_stages<S::H, S::UMAX, 2, OFF, INV>(a, rho);
       if constexpr (EPI == 1) {
-        static_assert(S::LB == G::P && DST == 1, "mirror epilogue: last pass to global");
+        static_assert(S::LB == G::P && DST != 0, "mirror epilogue: last pass to global");
         constexpr float scale = 1.0f / G::P;
 #pragma unroll
         for (int m = 0; m < S::UMAX / 2; ++m)
@@ -608,6 +609,15 @@ RD_HD void generic_slots(float (&a)[E], float* trow, int v, T* g, bool active) {
 #pragma unroll
         for (int m = S::UMAX / 2; m < S::UMAX; ++m)
           mirror_pair(a[OFF + 2 * (S::UMAX - 1 - m) + 1], a[OFF + 2 * m], scale);
+      }
+      if constexpr (DST == 2) {
+        if (active && gb != nullptr) {
+#pragma unroll
+          for (int m = 0; m < S::UMAX; ++m) {
+            a[OFF + 2 * m] += ld(gb + base + rho + m * S::H);
+            a[OFF + 2 * m + 1] += ld(gb + base - rho + (m + 1) * S::H);
+          }
+        }
       }
 #pragma unroll
       for (int m = 0; m < S::UMAX; ++m) {
@@ -621,14 +631,14 @@ RD_HD void generic_slots(float (&a)[E], float* trow, int v, T* g, bool active) {
         }
       }
     }
-    generic_slots<G, K, INV, SRC, DST, EPI, CI + 1>(a, trow, v, g, active);
+    generic_slots<G, K, INV, SRC, DST, EPI, CI + 1>(a, trow, v, g, active, gb);
   }
 }
 
 template <class G, int K, bool INV, int SRC, int DST, typename T, int EPI = 0>
-RD_HD void generic_pass(float* tile, int lrow, int v, T* g, bool active) {
+RD_HD void generic_pass(float* tile, int lrow, int v, T* g, bool active, const T* gb = nullptr) {
   float a[G::E];
-  generic_slots<G, K, INV, SRC, DST, EPI, 0>(a, tile + G::row_base(lrow), v, g, active);
+  generic_slots<G, K, INV, SRC, DST, EPI, 0>(a, tile + G::row_base(lrow), v, g, active, gb);
 }
 
 // The merged orbit of block beta of the row at tile row lrow in pass K: positions
@@ -636,7 +646,7 @@ RD_HD void generic_pass(float* tile, int lrow, int v, T* g, bool active) {
 // (M = 2) is already done; run its stages 4..N (or N..4 inverse). EPI = 1 applies the
 // mirror epilogue (pairs l, N - l; l = 0 and N/2 are their own mirrors).
 template <class G, int K, bool INV, int SRC, int DST, typename T, int EPI = 0>
-RD_HD void merged_orbit(float* tile, int lrow, int beta, T* g, bool active) {
+RD_HD void merged_orbit(float* tile, int lrow, int beta, T* g, bool active, const T* gb = nullptr) {
   using S = PassShape<G, K>;
   constexpr int SH = G::S;
   float a[S::N];
@@ -649,12 +659,18 @@ RD_HD void merged_orbit(float* tile, int lrow, int beta, T* g, bool active) {
   }
   stages_contig<4, S::N, S::N, 0, INV>(a);
   if constexpr (EPI == 1) {
-    static_assert(S::LB == G::P && DST == 1, "mirror epilogue: last pass to global");
+    static_assert(S::LB == G::P && DST != 0, "mirror epilogue: last pass to global");
     constexpr float scale = 1.0f / G::P;
     a[0] *= scale;
     a[S::N / 2] *= scale;
 #pragma unroll
     for (int l = 1; l < S::N / 2; ++l) mirror_pair(a[l], a[S::N - l], scale);
+  }
+  if constexpr (DST == 2) {
+    if (active && gb != nullptr) {
+#pragma unroll
+      for (int l = 0; l < S::N; ++l) a[l] += ld(gb + base + l * S::HH);
+    }
   }
 #pragma unroll
   for (int l = 0; l < S::N; ++l) {

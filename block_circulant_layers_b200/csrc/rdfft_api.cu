@@ -5,9 +5,11 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "rdfft.h"
+#include "adapter_plan.h"
 #include "internal.h"
 
 namespace {
@@ -139,6 +141,75 @@ cudaError_t noalloc_scratch(float** ptr) {
   *ptr = addr[dev];
   return cudaSuccess;
 }
+
+// ---- adapters of many requests
+
+struct Range {
+  const void* ptr;
+  size_t bytes;
+};
+
+// Any of the first `nout` ranges intersects another range.
+template <int N>
+bool outputs_overlap(const Range (&r)[N], int nout) {
+  for (int i = 0; i < nout; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (overlap(r[i].ptr, r[i].bytes, r[j].ptr, r[j].bytes)) return true;
+  return false;
+}
+
+template <int N>
+bool all_aligned16(const Range (&r)[N]) {
+  for (int i = 0; i < N; ++i)
+    if (!aligned16(r[i].ptr)) return false;
+  return true;
+}
+
+bool plan_sizes_ok(int64_t T, int n) {
+  return T >= 0 && T <= RDFFT_MAX_TOKENS && n >= 1 && n <= RDFFT_MAX_ADAPTERS;
+}
+size_t plan_bytes(int64_t T, int n) { return sizeof(int32_t) * (size_t)rdfft::plan_layout(T, n).words; }
+
+bool lora_sizes_ok(int64_t T, int K, int N, int r, int n) {
+  auto width = [](int w) { return w >= 8 && w <= 65536 && w % 8 == 0; };
+  return plan_sizes_ok(T, n) && width(K) && width(N) && r >= 8 && r <= 128 && r % 8 == 0;
+}
+
+int many_bwd_slices(int64_t T, int D, int p, int n, int dtype, int* slices) {
+  rdfft::CircMany a;
+  a.T = T, a.D = D, a.n = n;
+  rdfft::GcSink plan;
+  plan.plan_only = true;
+  const cudaError_t e = rdfft::launch_circ_many(2, a, p, dtype, nullptr, &plan);
+  *slices = plan.slices;
+  return finish(e);
+}
+
+// Argument checks shared by grad_norm and clip_grad_norm.
+int norm_args(const void* const* grads, const int64_t* numels, const int* dtypes, int count, float* norm,
+              void* workspace, size_t workspace_bytes) {
+  if (count < 0 || count > RDFFT_MAX_TENSORS) return RDFFT_EINVAL;
+  if (norm == nullptr || (count > 0 && (grads == nullptr || numels == nullptr || dtypes == nullptr)))
+    return RDFFT_ENULL;
+  for (int i = 0; i < count; ++i) {
+    if (!dtype_ok(dtypes[i])) return RDFFT_EDTYPE;
+    if (numels[i] < 0 || numels[i] > (INT64_MAX >> 16)) return RDFFT_EINVAL;
+    if (numels[i] > 0 && grads[i] == nullptr) return RDFFT_ENULL;
+    if (reinterpret_cast<uintptr_t>(grads[i]) % (dtypes[i] == RDFFT_F32 ? 4 : 2)) return RDFFT_EALIGN;
+  }
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return RDFFT_EALIGN;
+  const size_t need = sizeof(double) * (size_t)rdfft::grad_norm_ws_doubles(count);
+  if (need > 0) {
+    if (workspace == nullptr) return RDFFT_ENULL;
+    if (reinterpret_cast<uintptr_t>(workspace) % 8) return RDFFT_EALIGN;
+    if (workspace_bytes < need) return RDFFT_ESPACE;
+  }
+  return RDFFT_OK;
+}
+
+struct Span {
+  uintptr_t beg, end;
+};
 
 }  // namespace
 
@@ -285,18 +356,229 @@ int circ_bwd_x_tc(const void* g, const float* c_hat, void* grad_x, int64_t B, in
   return finish(rdfft::launch_circ_x_tc(g, c_hat, grad_x, B, true, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int adapter_plan_size(int64_t T, int n, int64_t* words) {
+  if (words == nullptr) return RDFFT_ENULL;
+  *words = 0;
+  if (!plan_sizes_ok(T, n)) return RDFFT_EINVAL;
+  *words = rdfft::plan_layout(T, n).words;
+  return RDFFT_OK;
+}
+
+int adapter_plan(const int32_t* ids, int64_t T, int n, int32_t* plan, rdfft_stream_t stream) {
+  if (!plan_sizes_ok(T, n)) return RDFFT_EINVAL;
+  if (plan == nullptr || (T > 0 && ids == nullptr)) return RDFFT_ENULL;
+  if (!aligned16(plan) || reinterpret_cast<uintptr_t>(ids) % 4) return RDFFT_EALIGN;
+  if (overlap(plan, plan_bytes(T, n), ids, sizeof(int32_t) * (size_t)T)) return RDFFT_EOVERLAP;
+  return finish(rdfft::launch_adapter_plan(ids, T, n, plan, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int lora_fwd(const void* x, const void* a, const void* b, const float* scale, const void* base, void* y, float* u,
+             const int32_t* plan, int64_t T, int K, int N, int r, int n, int dtype, rdfft_stream_t stream) {
+  if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
+  if (!lora_sizes_ok(T, K, N, r, n)) return RDFFT_EINVAL;
+  if (T == 0) return RDFFT_OK;
+  if (x == nullptr || a == nullptr || b == nullptr || y == nullptr || plan == nullptr) return RDFFT_ENULL;
+  const size_t es = dtype == RDFFT_F32 ? 4 : 2;
+  const Range args[] = {{y, es * T * N},
+                        {u, sizeof(float) * T * r},
+                        {x, es * T * K},
+                        {a, es * n * r * K},
+                        {b, es * n * r * N},
+                        {plan, plan_bytes(T, n)},
+                        {base == y ? nullptr : base, es * T * N}};
+  if (!all_aligned16(args) || reinterpret_cast<uintptr_t>(scale) % 4) return RDFFT_EALIGN;
+  if (outputs_overlap(args, 2) || overlap(scale, sizeof(float) * n, y, es * T * N) ||
+      overlap(scale, sizeof(float) * n, u, sizeof(float) * T * r))
+    return RDFFT_EOVERLAP;
+  return finish(rdfft::launch_lora_rows(false, x, a, b, scale, base, y, u, plan, T, K, N, r, n, dtype,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int lora_bwd(const void* g, const void* x, const void* a, const void* b, const float* scale, const float* u, float* v,
+             void* grad_x, float* grad_a, float* grad_b, const int32_t* plan, int64_t T, int K, int N, int r, int n,
+             int dtype, rdfft_stream_t stream) {
+  if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
+  if (!lora_sizes_ok(T, K, N, r, n)) return RDFFT_EINVAL;
+  if (grad_x == nullptr && grad_a == nullptr && grad_b == nullptr) return RDFFT_OK;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t es = dtype == RDFFT_F32 ? 4 : 2;
+  const size_t ga_bytes = sizeof(float) * n * r * K, gb_bytes = sizeof(float) * n * r * N;
+  if (T == 0) {                                        // no tokens: empty sums
+    if (!aligned16(grad_a) || !aligned16(grad_b)) return RDFFT_EALIGN;
+    if (overlap(grad_a, ga_bytes, grad_b, gb_bytes)) return RDFFT_EOVERLAP;
+    cudaError_t e = grad_a ? cudaMemsetAsync(grad_a, 0, ga_bytes, s) : cudaSuccess;
+    if (e == cudaSuccess && grad_b) e = cudaMemsetAsync(grad_b, 0, gb_bytes, s);
+    return finish(e);
+  }
+  const bool rows = grad_x != nullptr || grad_a != nullptr;
+  if (g == nullptr || plan == nullptr || (rows && b == nullptr) || (grad_x && a == nullptr) ||
+      (grad_a && (x == nullptr || v == nullptr)) || (grad_b && u == nullptr))
+    return RDFFT_ENULL;
+  const Range args[] = {{grad_x, es * T * K},
+                        {grad_a, ga_bytes},
+                        {grad_b, gb_bytes},
+                        {rows ? v : nullptr, sizeof(float) * T * r},
+                        {g, es * T * N},
+                        {x, es * T * K},
+                        {a, es * n * r * K},
+                        {b, es * n * r * N},
+                        {u, sizeof(float) * T * r},
+                        {plan, plan_bytes(T, n)},
+                        {scale, sizeof(float) * n}};
+  for (const Range& r16 : args)
+    if (r16.ptr != scale && !aligned16(r16.ptr)) return RDFFT_EALIGN;
+  if (reinterpret_cast<uintptr_t>(scale) % 4) return RDFFT_EALIGN;
+  if (outputs_overlap(args, 4)) return RDFFT_EOVERLAP;
+  cudaError_t e = cudaSuccess;
+  if (rows) e = rdfft::launch_lora_rows(true, g, b, a, scale, nullptr, grad_x, v, plan, T, N, K, r, n, dtype, s);
+  if (e == cudaSuccess && (grad_a || grad_b))
+    e = rdfft::launch_lora_wgrad(g, x, u, v, scale, grad_a, grad_b, plan, T, K, N, r, n, dtype, s);
+  return finish(e);
+}
+
+int circ_fwd_many(const void* x, const float* c_hat, const void* base, void* y, const int32_t* plan, int64_t T, int D,
+                  int p, int n, int dtype, rdfft_stream_t stream) {
+  if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
+  if (!layer_shape_ok(T, D, p) || !plan_sizes_ok(T, n)) return RDFFT_EINVAL;
+  if (T == 0) return RDFFT_OK;
+  if (x == nullptr || c_hat == nullptr || y == nullptr || plan == nullptr) return RDFFT_ENULL;
+  const size_t act = (size_t)T * D * (dtype == RDFFT_F32 ? 4 : 2);
+  const Range args[] = {{y, act}, {x, act}, {c_hat, n * gc_bytes(D, p)}, {plan, plan_bytes(T, n)},
+                        {base == y ? nullptr : base, act}};
+  if (!all_aligned16(args)) return RDFFT_EALIGN;
+  if (outputs_overlap(args, 1)) return RDFFT_EOVERLAP;
+  rdfft::CircMany c;
+  c.in = x, c.c_hat = c_hat, c.base = base, c.out = y, c.plan = plan;
+  c.T = T, c.D = D, c.n = n;
+  return finish(rdfft::launch_circ_many(0, c, p, dtype, reinterpret_cast<cudaStream_t>(stream), nullptr));
+}
+
+int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, size_t* bytes) {
+  if (bytes == nullptr) return RDFFT_ENULL;
+  *bytes = 0;
+  if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
+  if (!layer_shape_ok(T, D, p) || !plan_sizes_ok(T, n)) return RDFFT_EINVAL;
+  if (T == 0) return RDFFT_OK;
+  int slices = 0;
+  const int rc = many_bwd_slices(T, D, p, n, dtype, &slices);
+  if (rc == RDFFT_OK && slices > 1) *bytes = (size_t)slices * n * gc_bytes(D, p);
+  return rc;
+}
+
+int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x, float* grad_c, const int32_t* plan,
+                  int64_t T, int D, int p, int n, int dtype, void* workspace, size_t workspace_bytes,
+                  rdfft_stream_t stream) {
+  if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
+  if (!layer_shape_ok(T, D, p) || !plan_sizes_ok(T, n)) return RDFFT_EINVAL;
+  if (grad_x == nullptr && grad_c == nullptr) return RDFFT_OK;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t cb = n * gc_bytes(D, p);
+  if (T == 0) {
+    if (grad_c == nullptr) return RDFFT_OK;
+    if (!aligned16(grad_c)) return RDFFT_EALIGN;
+    return finish(cudaMemsetAsync(grad_c, 0, cb, s));
+  }
+  if (g == nullptr || plan == nullptr || (grad_x && c_hat == nullptr) || (grad_c && x == nullptr)) return RDFFT_ENULL;
+  size_t need = 0;
+  if (grad_c != nullptr) {
+    const int rc = circ_bwd_many_workspace_size(T, D, p, n, dtype, &need);
+    if (rc != RDFFT_OK) return rc;
+    if (need > 0 && workspace == nullptr) return RDFFT_ENULL;
+  }
+  const size_t act = (size_t)T * D * (dtype == RDFFT_F32 ? 4 : 2);
+  const Range args[] = {{grad_x, act}, {grad_c, cb}, {need ? workspace : nullptr, need}, {g, act}, {x, act},
+                        {c_hat, cb}, {plan, plan_bytes(T, n)}};
+  if (!all_aligned16(args)) return RDFFT_EALIGN;
+  if (workspace_bytes < need) return RDFFT_ESPACE;
+  if (outputs_overlap(args, 3)) return RDFFT_EOVERLAP;
+  rdfft::CircMany c;
+  c.c_hat = c_hat, c.plan = plan;
+  c.T = T, c.D = D, c.n = n;
+  cudaError_t e = cudaSuccess;
+  if (grad_c != nullptr) {
+    rdfft::GcSink sink;
+    sink.partial = need ? static_cast<float*>(workspace) : nullptr;
+    sink.partial_floats = (int64_t)(need / sizeof(float));
+    c.in = x, c.g = g, c.grad_c = grad_c;
+    e = rdfft::launch_circ_many(2, c, p, dtype, s, &sink);
+    if (e == cudaSuccess) e = rdfft::finish_grad_c(sink, grad_c, (int64_t)n * (D / p) * (D / p), p, s);
+  }
+  if (e == cudaSuccess && grad_x != nullptr) {
+    c.in = g, c.out = grad_x;
+    e = rdfft::launch_circ_many(1, c, p, dtype, s, nullptr);
+  }
+  return finish(e);
+}
+
+int grad_norm_workspace_size(int count, size_t* bytes) {
+  if (bytes == nullptr) return RDFFT_ENULL;
+  *bytes = 0;
+  if (count < 0 || count > RDFFT_MAX_TENSORS) return RDFFT_EINVAL;
+  *bytes = sizeof(double) * (size_t)rdfft::grad_norm_ws_doubles(count);
+  return RDFFT_OK;
+}
+
+int grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes, int count, float* norm,
+              void* workspace, size_t workspace_bytes, rdfft_stream_t stream) {
+  const int rc = norm_args(grads, numels, dtypes, count, norm, workspace, workspace_bytes);
+  if (rc != RDFFT_OK) return rc;
+  return finish(rdfft::launch_grad_norm(grads, nullptr, numels, dtypes, count, 0.0f, norm,
+                                        static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes, int count,
+                   float max_norm, float* norm, void* workspace, size_t workspace_bytes, rdfft_stream_t stream) {
+  if (!(max_norm >= 0.0f)) return RDFFT_EINVAL;
+  const int rc = norm_args(grads, numels, dtypes, count, norm, workspace, workspace_bytes);
+  if (rc != RDFFT_OK) return rc;
+  if (count > 0 && out == nullptr) return RDFFT_ENULL;
+  // outputs (and the norm and the workspace) sorted by address: neighbours must not overlap
+  Span spans[RDFFT_MAX_TENSORS + 2];
+  int ns = 0;
+  auto span_of = [](const void* ptr, size_t bytes) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(ptr);
+    return Span{b, b + bytes};
+  };
+  spans[ns++] = span_of(norm, sizeof(float));
+  if (count > 0) spans[ns++] = span_of(workspace, sizeof(double) * (size_t)rdfft::grad_norm_ws_doubles(count));
+  for (int i = 0; i < count; ++i) {
+    const size_t es = dtypes[i] == RDFFT_F32 ? 4 : 2;
+    if (numels[i] > 0 && out[i] == nullptr) return RDFFT_ENULL;
+    if (reinterpret_cast<uintptr_t>(out[i]) % es) return RDFFT_EALIGN;
+    if (numels[i] > 0) spans[ns++] = span_of(out[i], es * (size_t)numels[i]);
+  }
+  auto by_begin = [](const Span& a, const Span& b) { return a.beg < b.beg; };
+  std::sort(spans, spans + ns, by_begin);
+  for (int i = 1; i < ns; ++i)
+    if (spans[i].beg < spans[i - 1].end) return RDFFT_EOVERLAP;
+  for (int i = 0; i < count; ++i) {
+    if (numels[i] == 0) continue;
+    const Span in = span_of(grads[i], (dtypes[i] == RDFFT_F32 ? 4 : 2) * (size_t)numels[i]);
+    // the last span that begins before this tensor ends is the only one it can meet first
+    const Span* at = std::upper_bound(spans, spans + ns, Span{in.end - 1, 0}, by_begin);
+    if (at == spans) continue;
+    const Span& o = *(at - 1);
+    const bool own = out[i] == grads[i];
+    if (own ? o.beg != in.beg : o.end > in.beg) return RDFFT_EOVERLAP;
+  }
+  return finish(rdfft::launch_grad_norm(grads, out, numels, dtypes, count, max_norm, norm,
+                                        static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* rdfft_strerror(int code) {
   switch (code) {
     case RDFFT_OK: return "ok";
-    case RDFFT_EINVAL: return "invalid size: p must be a power of two in [2, 4096] (>= 64 for the layer), counts >= 0, D a multiple of p and <= RDFFT_MAX_D";
+    case RDFFT_EINVAL: return "invalid size: p must be a power of two in [2, 4096] (>= 64 for the layer), counts >= 0, D a multiple of p and <= RDFFT_MAX_D; adapters: 1 to 1024 of them, K and N multiples of 8 up to 65536, r a multiple of 8 up to 128; at most 4096 tensors, max_norm >= 0";
     case RDFFT_ENULL: return "a required pointer is NULL";
     case RDFFT_EALIGN: return "a pointer is not 16-byte aligned";
     case RDFFT_EDTYPE: return "dtype must be RDFFT_F32 (0) or RDFFT_BF16 (1)";
     case RDFFT_EOVERLAP: return "an output buffer overlaps an input buffer";
     case RDFFT_ETIMEOUT: return "a kernel's bounded wait for its data timed out; its rows were not transformed";
     case RDFFT_ESPACE:
-      return "the workspace is smaller than circ_bwd_workspace_size reports for this call (for "
-             "circ_bwd_deterministic_noalloc: the call needs more than its built-in 16 MiB of scratch)";
+      return "the workspace is smaller than circ_bwd_workspace_size (circ_bwd_many_workspace_size, "
+             "grad_norm_workspace_size) reports for this call (for circ_bwd_deterministic_noalloc: the call needs "
+             "more than its built-in 16 MiB of scratch)";
+    case RDFFT_EPLAN: return "a kernel was given an adapter plan made for other sizes; its outputs were not written";
     case RDFFT_ECUDA:
       snprintf(t_msg, sizeof(t_msg), "CUDA error while enqueuing: %s (%d)", cudaGetErrorString(t_last_cuda),
                (int)t_last_cuda);
@@ -306,18 +588,20 @@ const char* rdfft_strerror(int code) {
 }
 
 int rdfft_take_device_error(void) {
-  unsigned int flags = 0, tc_flags = 0, fused_flags = 0;
+  unsigned int flags = 0, tc_flags = 0, fused_flags = 0, plan_flags = 0;
   cudaError_t e = rdfft::take_rows_device_error(&flags);
   if (e == cudaSuccess) e = rdfft::take_tc_device_error(&tc_flags);
   if (e == cudaSuccess) e = rdfft::take_fused_device_error(&fused_flags);
+  if (e == cudaSuccess) e = rdfft::take_plan_device_error(&plan_flags);
   if (e != cudaSuccess) return finish(e);
-  return ((flags | tc_flags | fused_flags) & 1u) ? RDFFT_ETIMEOUT : RDFFT_OK;
+  if ((flags | tc_flags | fused_flags) & 1u) return RDFFT_ETIMEOUT;
+  return plan_flags ? RDFFT_EPLAN : RDFFT_OK;
 }
 
 int rdfft_selftest_wait_timeout(rdfft_stream_t stream) {
   return finish(rdfft::launch_wait_selftest(reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int rdfft_version(void) { return 110; }
+int rdfft_version(void) { return 120; }
 
 }  // extern "C"

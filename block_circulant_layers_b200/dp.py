@@ -37,6 +37,12 @@ class GradCBucket:
             self.flat.div_(world_size)
         return self.views
 
+    def clip(self, max_norm: float) -> torch.Tensor:
+        """Scales the bucket in place by min(1, max_norm / (norm + 1e-6)) and returns its norm (the
+        global norm of every grad_c of the step; call it after allreduce). CUDA buckets only."""
+        from . import _binding
+        return _binding.clip_grad_norm([self.flat], max_norm)
+
 
 def shard_tokens(total_tokens: int, rank: int, world_size: int) -> slice:
     """Contiguous token range of a rank (the first ranks take one more when uneven)."""

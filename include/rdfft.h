@@ -37,7 +37,7 @@
  *     anything is enqueued. RDFFT_ECUDA means a CUDA call failed when enqueuing;
  *     rdfft_strerror() then includes the CUDA message, which is kept per host
  *     thread. Empty work (rows == 0, images == 0 or B == 0) returns RDFFT_OK and
- *     enqueues nothing.
+ *     enqueues nothing (but a gradient that sums over tokens is zeroed, and a plan written).
  */
 #ifndef RDFFT_H
 #define RDFFT_H
@@ -59,14 +59,16 @@ enum {
 
 enum {
   RDFFT_OK = 0,
-  RDFFT_EINVAL = 1,   /* p not a power of two in [2, 4096] ([64, 4096] for the layer); negative count; D % p != 0; D too large */
+  RDFFT_EINVAL = 1,   /* p not a power of two in [2, 4096] ([64, 4096] for the layer); negative count; D % p != 0; D too large;
+                         adapter sizes outside what adapter_plan and lora_fwd accept; max_norm negative or NaN */
   RDFFT_ENULL = 2,    /* a required pointer is NULL */
   RDFFT_EALIGN = 3,   /* a pointer is not 16-byte aligned */
   RDFFT_EDTYPE = 4,   /* dtype is neither RDFFT_F32 nor RDFFT_BF16 */
   RDFFT_ECUDA = 5,    /* a CUDA call failed while enqueuing work */
   RDFFT_EOVERLAP = 6, /* an output buffer overlaps an input buffer it may not alias */
   RDFFT_ETIMEOUT = 7, /* reported by rdfft_take_device_error(): a bounded device wait gave up */
-  RDFFT_ESPACE = 8    /* the workspace is smaller than circ_bwd_workspace_size reports */
+  RDFFT_ESPACE = 8,   /* the workspace is smaller than the call's workspace-size function reports */
+  RDFFT_EPLAN = 9     /* reported by rdfft_take_device_error(): a kernel was given a plan of other sizes */
 };
 
 /* Largest feature size D accepted by circ_fwd / circ_bwd. */
@@ -275,6 +277,137 @@ int circ_fwd_tc(const void* x, const float* c_hat, void* y, int64_t B, int D, in
 int circ_bwd_x_tc(const void* g, const float* c_hat, void* grad_x, int64_t B, int D, int p, int dtype,
                   rdfft_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Adapters of many requests at once. A batch mixes tokens of requests that each use one of
+ * n adapters, or none; the adapters work beside a projection that all tokens share, whose
+ * result is given as `base`. The paper has no counterpart: it trains one adapter per layer.
+ *
+ * Largest number of adapters, and of tokens, of one call.
+ */
+#define RDFFT_MAX_ADAPTERS 1024
+#define RDFFT_MAX_TOKENS (1 << 30)
+
+/*
+ * adapter_plan_size -- int32 words of the plan of T tokens and n adapters. Enqueues nothing.
+ *   T in [0, RDFFT_MAX_TOKENS], n in [1, RDFFT_MAX_ADAPTERS].
+ */
+int adapter_plan_size(int64_t T, int n, int64_t* words);
+
+/*
+ * adapter_plan -- groups the tokens of a batch by adapter. The plan depends on the ids alone,
+ * so one plan serves every layer of a step, forward and backward.
+ *   ids  : T int32, the adapter of each token. A value outside [0, n) means no adapter.
+ *   plan : adapter_plan_size words, written; must not overlap ids. A plan may be made again
+ *          in place for other ids of the same T and n (inside a captured graph, too).
+ * Words of the plan that callers may read: [0] = T, [1] = n; [16, 16 + n + 2) = offsets; then,
+ * from 16 + (n + 2 rounded up to 4), T words of token order. Positions offsets[a] up to
+ * offsets[a + 1] of the order are the tokens of adapter a, ascending; a = n is the group
+ * without an adapter. The same on every run.
+ * A call that is given a plan of another T or n leaves its outputs unwritten, and
+ * rdfft_take_device_error then returns RDFFT_EPLAN.
+ */
+int adapter_plan(const int32_t* ids, int64_t T, int n, int32_t* plan, rdfft_stream_t stream);
+
+/*
+ * lora_fwd -- low-rank adapters: for token t with adapter k
+ *     u_t = A_k x_t,   y_t = base_t + scale_k B_k u_t,
+ * and y_t = base_t for a token without an adapter.
+ *   x     : T x K of `dtype`.   a : n x r x K of `dtype` (A).   b : n x N x r of `dtype` (B).
+ *   scale : n fp32, or NULL for 1.
+ *   base  : T x N of `dtype`, or NULL for zeros. It may be y itself (y += ...).
+ *   y     : T x N of `dtype`, written. Must not overlap any other argument (RDFFT_EOVERLAP).
+ *   u     : T x r fp32, written with A_k x_t (zeros without an adapter) for lora_bwd, or NULL.
+ *   plan  : the plan of the batch (same T and n).
+ *   K, N  : multiples of 8 in [8, 65536].   r : a multiple of 8 in [8, 128] (a smaller rank is
+ *           padded with zero rows of A and zero columns of B, which changes no result).
+ * Sums are fp32. In bf16, u enters the second product as the sum of two bf16 (16 mantissa bits)
+ * and y is rounded once. The result is the same on every run. An infinity or NaN stays within
+ * its token (or, in a weight, its adapter), where a bf16 result may be NaN instead of infinite.
+ */
+int lora_fwd(const void* x, const void* a, const void* b, const float* scale, const void* base, void* y, float* u,
+             const int32_t* plan, int64_t T, int K, int N, int r, int n, int dtype, rdfft_stream_t stream);
+
+/*
+ * lora_bwd -- gradients of lora_fwd for upstream gradient g = dL/dy (the gradient of base is g):
+ *     v_t = scale_k B_k^T g_t,   grad_x_t = A_k^T v_t,
+ *     grad_a[k] = sum_t v_t x_t^T,   grad_b[k] = scale_k sum_t g_t u_t^T   (over tokens of k).
+ *   g : T x N, x : T x K, a, b, scale, plan as lora_fwd.   u : T x r fp32, lora_fwd's.
+ *   grad_x : T x K of `dtype` (zeros for a token without an adapter), or NULL to skip it.
+ *   grad_a : n x r x K fp32, grad_b : n x N x r fp32, overwritten (zeros for an adapter
+ *            without tokens), or NULL to skip them.
+ *   v      : T x r fp32 workspace of the caller, needed with grad_a (else it may be NULL);
+ *            left holding v. Calls that share it must be ordered on one stream.
+ * What a skipped gradient alone needs may be NULL: x for grad_a, u for grad_b, a for grad_x.
+ * No output may overlap any other argument. Sums over tokens run in a fixed order: the
+ * gradients are the same on every run.
+ */
+int lora_bwd(const void* g, const void* x, const void* a, const void* b, const float* scale, const float* u, float* v,
+             void* grad_x, float* grad_a, float* grad_b, const int32_t* plan, int64_t T, int K, int N, int r, int n,
+             int dtype, rdfft_stream_t stream);
+
+/*
+ * circ_fwd_many -- circ_fwd with one of n block-circulant adapters per token:
+ *     y_t = base_t + W(c_k) x_t,   and y_t = base_t for a token without an adapter.
+ *   x     : T x D of `dtype`.   c_hat : n x q x q x p fp32 (circ_prepare or rdfft_fwd of the
+ *           parameters of each adapter).
+ *   base  : T x D of `dtype`, or NULL for zeros; it may be y itself.
+ *   y     : T x D of `dtype`, written. Must not overlap any other argument but base.
+ *   D, p  : as circ_fwd.   plan : the plan of the batch (same T and n).
+ */
+int circ_fwd_many(const void* x, const float* c_hat, const void* base, void* y, const int32_t* plan, int64_t T, int D,
+                  int p, int n, int dtype, rdfft_stream_t stream);
+
+/*
+ * circ_bwd_many_workspace_size -- device workspace, in bytes, of circ_bwd_many with grad_c for
+ * these sizes on the current device (0: none needed). Needs no GPU, as circ_bwd_workspace_size.
+ */
+int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, size_t* bytes);
+
+/*
+ * circ_bwd_many -- gradients of circ_fwd_many for upstream gradient g (the gradient of base is g):
+ *     grad_x_t = W(c_k)^T g_t (zeros for a token without an adapter),
+ *     grad_c[k] : as circ_bwd's grad_c, summed over the tokens of adapter k (zeros without any).
+ *   grad_x : T x D of `dtype`, or NULL.   grad_c : n x q x q x p fp32, overwritten, or NULL.
+ *   workspace : circ_bwd_many_workspace_size bytes, as circ_bwd_deterministic: the token slices
+ *               are summed in a fixed order, so grad_c is the same on every run.
+ */
+int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x, float* grad_c, const int32_t* plan,
+                  int64_t T, int D, int p, int n, int dtype, void* workspace, size_t workspace_bytes,
+                  rdfft_stream_t stream);
+
+/* Largest number of tensors of one grad_norm or clip_grad_norm call. */
+#define RDFFT_MAX_TENSORS 4096
+
+/*
+ * grad_norm_workspace_size -- device workspace, in bytes, of grad_norm and clip_grad_norm for
+ * `count` tensors. Enqueues nothing.
+ */
+int grad_norm_workspace_size(int count, size_t* bytes);
+
+/*
+ * grad_norm -- Euclidean norm of all elements of `count` tensors together, without a host sync.
+ *   grads, numels, dtypes : HOST arrays of `count` device pointers, element counts (>= 0) and
+ *            dtype codes (RDFFT_F32 or RDFFT_BF16, mixed freely); read before the call returns.
+ *            The tensors are dense and need only their element's alignment.
+ *   norm   : one fp32 on the device, written (0 for no elements).
+ *   workspace : grad_norm_workspace_size bytes, 8-byte aligned; overwritten. Calls that share
+ *            it must be ordered on one stream.
+ * Sums are double (of fp32 sums of 8 squares where those neither overflow nor underflow) and
+ * in a fixed order. A NaN or infinite element makes the norm NaN or infinite.
+ */
+int grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes, int count, float* norm,
+              void* workspace, size_t workspace_bytes, rdfft_stream_t stream);
+
+/*
+ * clip_grad_norm -- the norm as grad_norm, and out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)).
+ *   out      : HOST array of `count` device pointers; out[i] may be grads[i] (in place) and must
+ *              not overlap any other argument (RDFFT_EOVERLAP).
+ *   max_norm : >= 0. With a NaN norm every element becomes NaN; with an infinite one the finite
+ *              elements become 0 (max_norm finite).
+ */
+int clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes, int count,
+                   float max_norm, float* norm, void* workspace, size_t workspace_bytes, rdfft_stream_t stream);
+
 /*
  * rdfft_take_device_error -- the device error state of the transform kernels, then cleared.
  * No page has this; it is the library's failure detection. The row kernels move rows
@@ -287,7 +420,9 @@ int circ_bwd_x_tc(const void* g, const float* c_hat, void* grad_x, int64_t B, in
  * cores (their outputs are then left unwritten and their tensor memory is freed). This call
  * reads and clears that word for the current device. It synchronises with the device (a
  * cudaMemcpyFromSymbol), so call it between steps, not inside a captured graph.
- * Returns RDFFT_OK, RDFFT_ETIMEOUT, or RDFFT_ECUDA.
+ * The kernels of the many-adapter calls record here that they were given a plan of other
+ * sizes (RDFFT_EPLAN; a timeout is reported first).
+ * Returns RDFFT_OK, RDFFT_ETIMEOUT, RDFFT_EPLAN, or RDFFT_ECUDA.
  * After RDFFT_ETIMEOUT the contents of the rows of the launch that timed out are
  * undefined, and so are those of later launches in the stream until the stream has
  * been synchronised: a CTA whose wait gave up waits once more (again bounded) for its
