@@ -1,4 +1,5 @@
-"""ctypes binding of librdfft.so (argument marshalling only)."""
+"""Binding of librdfft.so (argument marshalling only): ctypes, and for the many-adapter calls and
+the gradient norm the C++ module _native.so (csrc/native_binding.cpp), which calls the same C ABI."""
 from __future__ import annotations
 
 import ctypes
@@ -18,6 +19,12 @@ if not os.path.exists(lib_path):
         "(the package has no non-CUDA fallback)")
 
 lib = ctypes.CDLL(lib_path)
+
+try:
+    from . import _native  # noqa: E402  (linked against librdfft.so beside it)
+except ImportError as e:
+    raise ImportError(f"the _native module next to {lib_path} is missing or does not load: build it with "
+                      "`python -m block_circulant_layers_b200.build`") from e
 
 _i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 lib.rdfft_fwd.argtypes = [_vp, _i64, _int, _int, _vp]
@@ -302,76 +309,35 @@ def circ_bwd_x_tc(g: torch.Tensor, c_hat: torch.Tensor, p: int, grad_x: torch.Te
 
 class AdapterPlan:
     """The tokens of a batch grouped by adapter (adapter_plan): one plan serves every layer of
-    a step. `order` (T,) and `offsets` (n + 2,) are int32 views of its buffer: positions
+    a step. `order` (T,) and `offsets` (n + 2,) are int32 views of its buffer `buf`: positions
     offsets[a]:offsets[a + 1] of the order are the tokens of adapter a, a = n those without."""
 
-    def __init__(self, T: int, n: int, device):
-        words = _i64()
-        _check(lib.adapter_plan_size(T, n, ctypes.byref(words)), "adapter_plan_size")
-        self.T, self.n = T, n
-        self.buf = torch.empty(words.value, dtype=torch.int32, device=device)
+    __slots__ = ("T", "n", "buf")
+
+    def __init__(self, T: int, n: int, buf: torch.Tensor):
+        self.T, self.n, self.buf = T, n, buf
 
     @property
     def offsets(self) -> torch.Tensor:
-        return self.buf[16:16 + self.n + 2]
+        return _native.plan_offsets(self.buf, self.T, self.n)
 
     @property
     def order(self) -> torch.Tensor:
-        at = 16 + (self.n + 2 + 3) // 4 * 4
-        return self.buf[at:at + self.T]
+        return _native.plan_order(self.buf, self.T, self.n)
 
 
 def adapter_plan(ids: torch.Tensor, n: int, out: AdapterPlan | None = None) -> AdapterPlan:
     """Plan of a batch whose token t uses adapter ids[t] of n (a value outside [0, n): none).
     ids: int32 (T,). `out` is a plan of the same T and n to make again in place."""
-    _cuda_dense(ids, "ids")
-    if ids.dtype != torch.int32 or ids.dim() != 1:
-        raise TypeError("ids must be a one-dimensional int32 tensor")
-    T = ids.numel()
     if out is None:
-        out = AdapterPlan(T, n, ids.device)
-    elif out.T != T or out.n != n or out.buf.device != ids.device:
+        code, buf = _native.adapter_plan(ids, n, None)
+        _check(code, "adapter_plan")
+        return AdapterPlan(ids.numel(), n, buf)
+    if out.T != ids.numel() or out.n != n or out.buf.device != ids.device:
         raise ValueError("out must be a plan of the same number of tokens and adapters on the same device")
-    else:
-        torch.autograd.graph.increment_version(out.buf)      # a backward pass that saved it must not use it now
-    with torch.cuda.device(ids.device):
-        _check(lib.adapter_plan(ids.data_ptr(), T, n, out.buf.data_ptr(), _stream(ids)), "adapter_plan")
+    torch.autograd.graph.increment_version(out.buf)          # a backward pass that saved it must not use it now
+    _check(_native.adapter_plan(ids, n, out.buf)[0], "adapter_plan")
     return out
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _like(t, name: str, shape, dtype, device, make: bool = False):
-    """t checked against shape, dtype and device; None stays None, or becomes a new tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device) if make else None
-    _cuda_dense(t, name)
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, dtype {dtype} and be on {device}")
-    return t
-
-
-def _plan_for(plan: AdapterPlan, rows: torch.Tensor, n: int, name: str):
-    if not isinstance(plan, AdapterPlan):
-        raise TypeError("plan must be an AdapterPlan (adapter_plan)")
-    if plan.T != rows.numel() // max(rows.shape[-1], 1) or plan.n != n or plan.buf.device != rows.device:
-        raise ValueError(f"the plan is for {plan.T} tokens and {plan.n} adapters on {plan.buf.device}, not for {name}")
-
-
-def _lora_weights(x, a, b, plan, scale):
-    for t, name in ((x, "x"), (a, "a"), (b, "b")):
-        _cuda_dense(t, name)
-    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] \
-            or x.dim() < 1 or x.shape[-1] != a.shape[2]:
-        raise ValueError("x must have shape (..., K), a (n, r, K) and b (n, N, r)")
-    if a.dtype != x.dtype or b.dtype != x.dtype or a.device != x.device or b.device != x.device:
-        raise ValueError("a and b must match x in dtype and device")
-    n, r, K = a.shape
-    _plan_for(plan, x, n, "x and a")
-    _like(scale, "scale", (n,), torch.float32, x.device)
-    return plan.T, K, b.shape[1], r, n
 
 
 def lora_fwd(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: AdapterPlan, scale: torch.Tensor | None = None,
@@ -381,14 +347,8 @@ def lora_fwd(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: AdapterPla
 
     x (..., K), a (n, r, K), b (n, N, r) and base (..., N) of one dtype; scale (n,) float32.
     y may be base (in place). u (T, r) float32, if given, receives a_k x_t for lora_bwd."""
-    T, K, N, r, n = _lora_weights(x, a, b, plan, scale)
-    shape = x.shape[:-1] + (N,)
-    _like(base, "base", shape, x.dtype, x.device)
-    y = _like(y, "y", shape, x.dtype, x.device, make=True)
-    _like(u, "u", (T, r), torch.float32, x.device)
-    with torch.cuda.device(x.device):
-        _check(lib.lora_fwd(x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), _ptr(base), y.data_ptr(), _ptr(u),
-                            plan.buf.data_ptr(), T, K, N, r, n, _dtype_code(x), _stream(x)), "lora_fwd")
+    code, y = _native.lora_fwd(x, a, b, plan.buf, plan.T, plan.n, scale, base, y, u)
+    _check(code, "lora_fwd")
     return y
 
 
@@ -400,34 +360,10 @@ def lora_bwd(g: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     """(grad_x, grad_a, grad_b) of lora_fwd for upstream gradient g (..., N); grad_a and grad_b
     are float32. u (T, r) is lora_fwd's (it may be None without grad_b). The (T, r) float32
     workspace is taken from `workspace` if given, else allocated here."""
-    T, K, N, r, n = _lora_weights(x, a, b, plan, scale)
-    _cuda_dense(g, "g")
-    _like(g, "g", x.shape[:-1] + (N,), x.dtype, x.device)
-    _like(u, "u", (T, r), torch.float32, x.device)
-    if need_grad_b and u is None:
-        raise ValueError("grad_b needs the u that lora_fwd writes")
-    f32, dev = torch.float32, x.device
-    grad_x = _like(grad_x, "grad_x", x.shape, x.dtype, dev, make=True) if need_grad_x else None
-    grad_a = _like(grad_a, "grad_a", a.shape, f32, dev, make=True) if need_grad_a else None
-    grad_b = _like(grad_b, "grad_b", b.shape, f32, dev, make=True) if need_grad_b else None
-    v = _like(workspace, "workspace", (T, r), f32, dev, make=need_grad_a)
-    with torch.cuda.device(dev):
-        _check(lib.lora_bwd(g.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), _ptr(u), _ptr(v),
-                            _ptr(grad_x), _ptr(grad_a), _ptr(grad_b), plan.buf.data_ptr(), T, K, N, r, n,
-                            _dtype_code(x), _stream(x)), "lora_bwd")
+    code, grad_x, grad_a, grad_b = _native.lora_bwd(g, x, a, b, plan.buf, plan.T, plan.n, u, scale, need_grad_x,
+                                                    need_grad_a, need_grad_b, grad_x, grad_a, grad_b, workspace)
+    _check(code, "lora_bwd")
     return grad_x, grad_a, grad_b
-
-
-def _circ_many(x, c_hat, p, plan):
-    _cuda_dense(x, "x")
-    _cuda_dense(c_hat, "c_hat")
-    if c_hat.dtype != torch.float32 or c_hat.device != x.device:
-        raise TypeError("c_hat must be float32 on x's device")
-    if c_hat.dim() != 4 or c_hat.shape[1] != c_hat.shape[2] or c_hat.shape[3] != p or x.dim() < 1 \
-            or x.shape[-1] != c_hat.shape[1] * p:
-        raise ValueError("x must have shape (..., q * p) and c_hat (n, q, q, p)")
-    _plan_for(plan, x, c_hat.shape[0], "x and c_hat")
-    return plan.T, x.shape[-1], c_hat.shape[0]
 
 
 def circ_fwd_many(x: torch.Tensor, c_hat: torch.Tensor, p: int, plan: AdapterPlan, base: torch.Tensor | None = None,
@@ -436,12 +372,8 @@ def circ_fwd_many(x: torch.Tensor, c_hat: torch.Tensor, p: int, plan: AdapterPla
 
     x and base (..., D) of one dtype; c_hat (n, q, q, p) float32, each adapter's circ_prepare
     (or rdfft_fwd of the (n, q, q, p) parameters). y may be base (in place)."""
-    T, D, n = _circ_many(x, c_hat, p, plan)
-    _like(base, "base", x.shape, x.dtype, x.device)
-    y = _like(y, "y", x.shape, x.dtype, x.device, make=True)
-    with torch.cuda.device(x.device):
-        _check(lib.circ_fwd_many(x.data_ptr(), c_hat.data_ptr(), _ptr(base), y.data_ptr(), plan.buf.data_ptr(), T, D, p,
-                                 n, _dtype_code(x), _stream(x)), "circ_fwd_many")
+    code, y = _native.circ_fwd_many(x, c_hat, p, plan.buf, plan.T, plan.n, base, y)
+    _check(code, "circ_fwd_many")
     return y
 
 
@@ -451,82 +383,26 @@ def circ_bwd_many(g: torch.Tensor, x: torch.Tensor, c_hat: torch.Tensor, p: int,
     """(grad_x, grad_c) of circ_fwd_many for upstream gradient g; grad_c (n, q, q, p) float32 is
     the same on every run. The workspace (circ_bwd_many_workspace_size bytes) is taken from
     `workspace` if given, else allocated here."""
-    T, D, n = _circ_many(x, c_hat, p, plan)
-    _cuda_dense(g, "g")
-    _like(g, "g", x.shape, x.dtype, x.device)
-    grad_x = _like(grad_x, "grad_x", x.shape, x.dtype, x.device, make=True) if need_grad_x else None
-    grad_c = _like(grad_c, "grad_c", c_hat.shape, torch.float32, x.device, make=True) if need_grad_c else None
-    with torch.cuda.device(x.device):
-        if need_grad_c:
-            need = ctypes.c_size_t()
-            _check(lib.circ_bwd_many_workspace_size(T, D, p, n, _dtype_code(x), ctypes.byref(need)),
-                   "circ_bwd_many_workspace_size")
-            if workspace is None and need.value:
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        if workspace is not None:
-            _cuda_dense(workspace, "workspace")
-        size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.circ_bwd_many(g.data_ptr(), x.data_ptr(), c_hat.data_ptr(), _ptr(grad_x), _ptr(grad_c),
-                                 plan.buf.data_ptr(), T, D, p, n, _dtype_code(x), _ptr(workspace), size, _stream(x)),
-               "circ_bwd_many")
+    code, grad_x, grad_c = _native.circ_bwd_many(g, x, c_hat, p, plan.buf, plan.T, plan.n, grad_x, grad_c, need_grad_x,
+                                                 need_grad_c, workspace)
+    _check(code, "circ_bwd_many")
     return grad_x, grad_c
-
-
-_CODES = {torch.float32: RDFFT_F32, torch.bfloat16: RDFFT_BF16}
-
-
-def _tensor_list(tensors, name: str):
-    """Host arrays (pointers, element counts, dtype codes) of a list of CUDA tensors."""
-    for t in tensors:
-        if not t.is_cuda or not t.is_contiguous() or t.dtype not in _CODES:
-            raise TypeError(f"{name} must be contiguous float32 or bfloat16 CUDA tensors")
-    if len({t.get_device() for t in tensors}) > 1:
-        raise ValueError(f"{name} must be on one device")
-    m = len(tensors)
-    return ((_vp * m)(*[t.data_ptr() for t in tensors]), (_i64 * m)(*[t.numel() for t in tensors]),
-            (_int * m)(*[_CODES[t.dtype] for t in tensors]))
-
-
-def _norm_call(tensors, device, call, where: str):
-    need = ctypes.c_size_t()
-    _check(lib.grad_norm_workspace_size(len(tensors), ctypes.byref(need)), "grad_norm_workspace_size")
-    # the norm stands behind the workspace
-    buf = torch.empty(need.value // 4 + 1, dtype=torch.float32, device=device)
-    norm = buf[need.value // 4]
-    with torch.cuda.device(device):
-        _check(call(norm.data_ptr(), buf.data_ptr(), need.value, torch.cuda.current_stream(device).cuda_stream), where)
-    return norm
 
 
 def grad_norm(tensors) -> torch.Tensor:
     """Euclidean norm of all elements of a list of float32 or bfloat16 CUDA tensors together, as
     a 0-dim float32 tensor on their device (no host sync)."""
-    tensors = list(tensors)
-    if not tensors:
-        raise ValueError("grad_norm needs at least one tensor")
-    ptrs, numels, codes = _tensor_list(tensors, "tensors")
-    return _norm_call(tensors, tensors[0].device,
-                      lambda norm, ws, size, s: lib.grad_norm(ptrs, numels, codes, len(tensors), norm, ws, size, s),
-                      "grad_norm")
+    code, norm = _native.norm(list(tensors), False, 0.0, None)
+    _check(code, "grad_norm")
+    return norm
 
 
 def clip_grad_norm(tensors, max_norm: float, out=None) -> torch.Tensor:
     """The norm of grad_norm; every tensor is scaled by min(1, max_norm / (norm + 1e-6)), in place
     or into the matching tensor of `out` (same element count and dtype). No host sync."""
-    tensors = list(tensors)
-    if not tensors:
-        raise ValueError("clip_grad_norm needs at least one tensor")
-    ptrs, numels, codes = _tensor_list(tensors, "tensors")
-    optrs = ptrs
-    if out is not None:
-        out = list(out)
-        optrs, onumels, ocodes = _tensor_list(out, "out")
-        if len(out) != len(tensors) or list(onumels) != list(numels) or list(ocodes) != list(codes) \
-                or out[0].device != tensors[0].device:
-            raise ValueError("out must match the tensors in number, element counts, dtypes and device")
-    return _norm_call(tensors, tensors[0].device,
-                      lambda norm, ws, size, s: lib.clip_grad_norm(ptrs, optrs, numels, codes, len(tensors), max_norm,
-                                                                   norm, ws, size, s), "clip_grad_norm")
+    code, norm = _native.norm(list(tensors), True, max_norm, None if out is None else list(out))
+    _check(code, "clip_grad_norm")
+    return norm
 
 
 def take_device_error() -> int:

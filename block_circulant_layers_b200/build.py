@@ -5,11 +5,13 @@
 * librdfft.so         -- the C ABI of include/rdfft.h with the sm_100a kernels
                          (nvcc -gencode arch=compute_100a,code=sm_100a; cross-compiles
                          on a machine without a GPU).
+* _native.so          -- the C++ binding of the many-adapter calls over that ABI (g++, torch's
+                         headers; linked against librdfft.so beside it).
 * librdfft_hostemu.so -- the same per-thread rdFFT pass code compiled for the host
                          (g++), used by the CPU tests to check the kernels' index
                          logic and arithmetic without a GPU.
 
-Both land next to this file so that they travel with the source tree.
+All land next to this file so that they travel with the source tree.
 """
 from __future__ import annotations
 
@@ -28,6 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 
 LIB = os.path.join(PKG, "librdfft.so")
+NATIVE = os.path.join(PKG, "_native.so")
 EMU = os.path.join(PKG, "librdfft_hostemu.so")
 
 CU_SOURCES = ["rdfft_api.cu", "rdfft_kernels.cu", "rdfft2d_kernels.cu", "convert_kernels.cu", "circ_launch.cu",
@@ -53,6 +56,17 @@ def _newest_input_mtime() -> float:
 
 def _up_to_date(target: str) -> bool:
     return os.path.exists(target) and os.path.getmtime(target) >= _newest_input_mtime()
+
+
+def _object_current(obj: str) -> bool:
+    """An object is newer than every file its compilation read (nvcc's dependency file) and this one."""
+    dep = obj[:-2] + ".d"
+    if not (os.path.exists(obj) and os.path.exists(dep)):
+        return False
+    with open(dep) as f:
+        paths = f.read().replace("\\\n", " ").split(":", 1)[1].split()
+    made = os.path.getmtime(obj)
+    return all(os.path.exists(p) and os.path.getmtime(p) <= made for p in paths + [os.path.abspath(__file__)])
 
 
 def _run(cmd, verbose):
@@ -87,8 +101,9 @@ def build_lib(force=False, verbose=False, ptxas_info=False) -> str:
     for src in CU_SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         objs.append(obj)
-        cmds.append([nvcc, "-c", os.path.join(CSRC, src), "-o", obj] + flags)
-    with cf.ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 4)) as ex:
+        if force or not _object_current(obj):
+            cmds.append([nvcc, "-c", os.path.join(CSRC, src), "-o", obj, "-MD", "-MF", obj[:-2] + ".d"] + flags)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 4))) as ex:
         outs = list(ex.map(lambda c: _run(c, verbose), cmds))
     if ptxas_info:
         for o in outs:
@@ -97,6 +112,28 @@ def build_lib(force=False, verbose=False, ptxas_info=False) -> str:
     _run([nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"], verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_native(force=False, verbose=False) -> str:
+    build_lib(force=force, verbose=verbose)
+    if not force and _up_to_date(NATIVE):
+        return NATIVE
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE,
+                                           CSRC]
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + ".tmp"
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+         + [f"-I{p}" for p in inc]
+         + [os.path.join(CSRC, "native_binding.cpp"), "-o", tmp, "-L", PKG, "-l:librdfft.so", "-L", torch_lib,
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 def build_emulator(force=False, verbose=False) -> str:
@@ -113,6 +150,7 @@ def build_emulator(force=False, verbose=False) -> str:
 
 def build(force=False, verbose=False, emulator=True) -> None:
     build_lib(force=force, verbose=verbose)
+    build_native(verbose=verbose)
     if emulator:
         build_emulator(force=force, verbose=verbose)
 
@@ -125,6 +163,7 @@ def main(argv=None) -> int:
     ap.add_argument("-v", "--verbose", action="store_true")
     a = ap.parse_args(argv)
     build_lib(force=a.force or a.ptxas_info, verbose=a.verbose, ptxas_info=a.ptxas_info)
+    build_native(verbose=a.verbose)
     if not a.no_emulator:
         build_emulator(force=a.force, verbose=a.verbose)
     print(LIB)

@@ -1,12 +1,13 @@
 // Global norm of many tensors, and the tensors clipped by it:
 //   norm = sqrt(sum over all elements of g^2),  out = g * min(1, max_norm / (norm + 1e-6)).
 //
-// Two launches for up to kMaxTensors tensors. k_norm_partial: every CTA sums the squares of a
-// fixed share of the elements (the tensors' 16-byte pieces, numbered through) and stores one
-// double; k_norm_finish: every CTA adds all those partial sums in the same order, so the norm
-// is the same on every run and needs no counter or zeroed state, and then scales its share.
-// Bound by memory: 1 read for the norm, 1 read and 1 write for the scaling, of which the
-// second read comes from L2 as far as the tensors fit it.
+// Two launches for up to kMost tensors. The elements are cut into blocks of 16384 of one tensor.
+// k_norm_partial: a CTA sums the squares of every grid-th block and stores one double;
+// k_norm_finish: every CTA adds all those partial sums in the same order, so the norm is the
+// same on every run and needs no counter or zeroed state, and then scales its blocks. It takes
+// them in the opposite order: what the first pass read last is still in L2.
+// Bound by memory: 1 read for the norm, 1 read and 1 write for the scaling, less what L2 keeps.
+// A thread requests its 8 pieces of 16 bytes (16 in fp32) of a block before it uses the first.
 //
 // Squares of 8 elements are added in fp32 and those sums in double, so neither long sums nor
 // many tensors lose bits; a sum of 8 that overflows fp32 or falls to its smallest range is
@@ -23,25 +24,29 @@ namespace rdfft {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTensors = 512;               // per launch: 20 bytes each of kernel parameters
+constexpr int kFew = 64, kMost = 1024;         // tensors per launch (kernel parameters: 32764 bytes at most)
 constexpr int kMaxGrid = 592;                  // partial sums per launch
+constexpr int kPer = 8;                        // units of 8 elements per thread and block
+constexpr int kUnits = kPer * kThreads;        // units per block
 
-// One launch's tensors. Work is numbered in units of 8 elements; units of tensor i are
-// [first[i], first[i + 1]).
+// One launch's tensors: tensor i has the blocks [first[i], first[i + 1]), and its last block
+// ends `tail` elements before its end.
+template <int CAP>
 struct Tensors {
-  const void* in[kMaxTensors];
-  void* out[kMaxTensors];
-  int64_t numel[kMaxTensors];
-  int64_t first[kMaxTensors + 1];
-  uint8_t bf16[kMaxTensors];
+  const void* in[CAP];
+  void* out[CAP];
+  int64_t first[CAP + 1];
+  uint16_t tail[CAP];
+  uint8_t bf16[CAP];
   int count;
 };
 
-__device__ __forceinline__ int tensor_of(const Tensors& t, int64_t unit) {
-  int lo = 0, hi = t.count;                    // first[lo] <= unit < first[hi]
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Tensors<CAP>& t, int64_t block) {
+  int lo = 0, hi = t.count;                    // first[lo] <= block < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (t.first[mid] <= unit) lo = mid; else hi = mid;
+    if (t.first[mid] <= block) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -78,10 +83,10 @@ __device__ __forceinline__ void store_unit(void* p, bool bf16, int64_t e, int64_
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         u[i] = (uint32_t)from_f32<bf16_t>(v[2 * i]) | (uint32_t)from_f32<bf16_t>(v[2 * i + 1]) << 16;
-      *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+      __stcs(reinterpret_cast<uint4*>(at), make_uint4(u[0], u[1], u[2], u[3]));
     } else {
-      reinterpret_cast<float4*>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      __stcs(reinterpret_cast<float4*>(at), make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<float4*>(at) + 1, make_float4(v[4], v[5], v[6], v[7]));
     }
     return;
   }
@@ -106,31 +111,84 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-__global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant__ Tensors t,
+// Calls use(unit's first element, its 8 values) for this thread's units of one block, loads
+// first. LAST: streaming loads, for data that no one reads again.
+template <bool LAST, typename Use>
+__device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, int64_t n, Use use) {
+  const char* base = static_cast<const char*>(p) + e0 * (bf16 ? 2 : 4);
+  if (n - e0 < 8 * kUnits || (reinterpret_cast<uintptr_t>(base) & 15) != 0) {
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t e = e0 + 8 * (threadIdx.x + kThreads * i);
+      if (e >= n) return;
+      float v[8];
+      load_unit(p, bf16, e, n, v);
+      use(e, v);
+    }
+    return;
+  }
+  const float4* src = reinterpret_cast<const float4*>(base);
+  auto get = [](const float4* a) { return LAST ? __ldcs(a) : *a; };
+  if (bf16) {
+    float4 w[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) w[i] = get(src + threadIdx.x + kThreads * i);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t u[4] = {__float_as_uint(w[i].x), __float_as_uint(w[i].y), __float_as_uint(w[i].z),
+                             __float_as_uint(w[i].w)};
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(u[k] << 16);
+        v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+      }
+      use(e0 + 8 * (threadIdx.x + kThreads * i), v);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4 w[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        w[i] = get(src + 2 * (threadIdx.x + kThreads * (kPer / 2 * h + i / 2)) + (i & 1));
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) {
+        const float4 a = w[2 * i], b = w[2 * i + 1];
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        use(e0 + 8 * (threadIdx.x + kThreads * (kPer / 2 * h + i)), v);
+      }
+    }
+  }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant__ Tensors<CAP> t,
                                                            double* __restrict__ partial) {
   griddep_wait();
-  const int64_t units = t.first[t.count], step = (int64_t)gridDim.x * kThreads;
+  const int64_t blocks = t.first[t.count];
   double sum = 0.0;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
-    const int i = tensor_of(t, u);
-    float v[8];
-    load_unit(t.in[i], t.bf16[i], 8 * (u - t.first[i]), t.numel[i], v);
-    float s = 0.0f;
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const int i = tensor_of(t, b);
+    const int64_t n = 8 * kUnits * (t.first[i + 1] - t.first[i]) - t.tail[i];
+    each_unit<false>(t.in[i], t.bf16[i], 8 * kUnits * (b - t.first[i]), n, [&](int64_t, const float (&v)[8]) {
+      float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
-    if (s > 1e-30f && s < 1e38f) {
-      sum += s;
-    } else {
+      for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
+      if (s > 1e-30f && s < 1e38f) {
+        sum += s;
+      } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum += (double)v[k] * (double)v[k];
-    }
+        for (int k = 0; k < 8; ++k) sum += (double)v[k] * (double)v[k];
+      }
+    });
   }
   griddep_launch_dependents();
   const double s = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(kThreads) k_norm_finish(const __grid_constant__ Tensors t,
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_norm_finish(const __grid_constant__ Tensors<CAP> t,
                                                           const double* __restrict__ partial, int npartial,
                                                           float max_norm, float* norm) {
   griddep_wait();
@@ -138,71 +196,74 @@ __global__ void __launch_bounds__(kThreads) k_norm_finish(const __grid_constant_
   for (int i = threadIdx.x; i < npartial; i += kThreads) s += partial[i];
   const float nrm = (float)sqrt(block_sum(s));
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
-  if (t.count == 0) return;
   // a NaN norm keeps the coefficient NaN, an infinite one makes it 0
   const float ratio = max_norm / (nrm + 1e-6f);
   const float coef = ratio > 1.0f ? 1.0f : ratio;
-  const int64_t units = t.first[t.count], step = (int64_t)gridDim.x * kThreads;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
-    const int i = tensor_of(t, u);
-    const int64_t e = 8 * (u - t.first[i]);
-    float v[8];
-    load_unit(t.in[i], t.bf16[i], e, t.numel[i], v);
+  const int64_t blocks = t.first[t.count];
+  for (int64_t r = blockIdx.x; r < blocks; r += gridDim.x) {
+    const int64_t b = blocks - 1 - r;
+    const int i = tensor_of(t, b);
+    const int64_t n = 8 * kUnits * (t.first[i + 1] - t.first[i]) - t.tail[i];
+    each_unit<true>(t.in[i], t.bf16[i], 8 * kUnits * (b - t.first[i]), n, [&](int64_t e, float (&v)[8]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= coef;
-    store_unit(t.out[i], t.bf16[i], e, t.numel[i], v);
+      for (int k = 0; k < 8; ++k) v[k] *= coef;
+      store_unit(t.out[i], t.bf16[i], e, n, v);
+    });
   }
   griddep_launch_dependents();
 }
 
-int grid_of(int64_t units) {
-  const int64_t b = (units + kThreads - 1) / kThreads;
-  return (int)(b < 1 ? 1 : (b < kMaxGrid ? b : kMaxGrid));
-}
+int grid_of(int64_t blocks) { return (int)(blocks < 1 ? 1 : (blocks < kMaxGrid ? blocks : kMaxGrid)); }
 
-}  // namespace
-
-int64_t grad_norm_ws_doubles(int count) {
-  return (int64_t)((count + kMaxTensors - 1) / kMaxTensors) * kMaxGrid;
-}
-
-cudaError_t launch_grad_norm(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes,
-                             int count, float max_norm, float* norm, double* ws, cudaStream_t s) {
-  // the largest number of parameters a kernel takes is 32764 bytes
-  static_assert(sizeof(Tensors) <= 32000, "kernel parameters");
-  Tensors t;
+template <int CAP>
+cudaError_t run(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes, int count,
+                float max_norm, float* norm, double* ws, cudaStream_t s) {
+  static_assert(sizeof(Tensors<CAP>) + 64 <= 32764, "kernel parameters");
+  Tensors<CAP> t;
   auto gather = [&](int i0) {
     t.count = 0;
     t.first[0] = 0;
-    for (int i = i0; i < count && i < i0 + kMaxTensors; ++i) {
+    for (int i = i0; i < count && i < i0 + CAP; ++i) {
       const int k = t.count++;
+      const int64_t blocks = (numels[i] + 8 * kUnits - 1) / (8 * kUnits);
       t.in[k] = grads[i];
       t.out[k] = out ? out[i] : nullptr;
-      t.numel[k] = numels[i];
       t.bf16[k] = dtypes[i] == 1;
-      t.first[k + 1] = t.first[k] + (numels[i] + 7) / 8;
+      t.tail[k] = (uint16_t)(8 * kUnits * blocks - numels[i]);
+      t.first[k + 1] = t.first[k] + blocks;
     }
   };
   int npartial = 0;
-  for (int i = 0; i < count; i += kMaxTensors) {
+  for (int i = 0; i < count; i += CAP) {
     gather(i);
     const int grid = grid_of(t.first[t.count]);
-    const cudaError_t e = launch_pdl(k_norm_partial, dim3(grid), dim3(kThreads), 0, s, t, ws + npartial);
+    const cudaError_t e = launch_pdl(k_norm_partial<CAP>, dim3(grid), dim3(kThreads), 0, s, t, ws + npartial);
     if (e != cudaSuccess) return e;
     npartial += grid;
   }
   if (out == nullptr || count == 0) {
-    t.count = 0;
+    t.count = 0;                                   // no blocks: the norm alone
     t.first[0] = 0;
-    return launch_pdl(k_norm_finish, dim3(1), dim3(kThreads), 0, s, t, ws, npartial, max_norm, norm);
+    return launch_pdl(k_norm_finish<CAP>, dim3(1), dim3(kThreads), 0, s, t, ws, npartial, max_norm, norm);
   }
-  for (int i = 0; i < count; i += kMaxTensors) {
-    if (count > kMaxTensors) gather(i);
-    const cudaError_t e = launch_pdl(k_norm_finish, dim3(grid_of(t.first[t.count])), dim3(kThreads), 0, s, t, ws,
+  for (int i = 0; i < count; i += CAP) {
+    if (count > CAP) gather(i);
+    const cudaError_t e = launch_pdl(k_norm_finish<CAP>, dim3(grid_of(t.first[t.count])), dim3(kThreads), 0, s, t, ws,
                                      npartial, max_norm, i == 0 ? norm : static_cast<float*>(nullptr));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+int64_t grad_norm_ws_doubles(int count) { return (int64_t)((count + kMost - 1) / kMost) * kMaxGrid; }
+
+cudaError_t launch_grad_norm(const void* const* grads, void* const* out, const int64_t* numels, const int* dtypes,
+                             int count, float max_norm, float* norm, double* ws, cudaStream_t s) {
+  // few tensors: a tenth of the parameters to copy per launch
+  if (count <= kFew) return run<kFew>(grads, out, numels, dtypes, count, max_norm, norm, ws, s);
+  return run<kMost>(grads, out, numels, dtypes, count, max_norm, norm, ws, s);
 }
 
 }  // namespace rdfft
