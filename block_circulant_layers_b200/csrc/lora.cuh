@@ -84,6 +84,30 @@ struct LoraWgrad {
   PlanView plan;
 };
 
+// The weight gradients share the batch evenly: CTA `rank` of a cluster of C takes an equal part
+// [lo, hi) of the plan's 64-token tiles, whatever adapters they belong to. (A CTA per adapter
+// would leave the launch to the adapter with most tokens.) Tiles lie in the order of their
+// positions, so a tile ends where the next begins, and consecutive tiles of one adapter are one
+// sum. kWindow tiles and their neighbours are looked up at a time.
+constexpr int kWindow = 254;
+struct TileShare {
+  int lo, hi, all, end;                     // of `all` tiles with an adapter, whose positions end at `end`
+  __device__ __forceinline__ TileShare(const PlanView& v, unsigned rank, unsigned C) {
+    end = __ldg(v.offsets + v.n);
+    const int none = __ldg(v.offsets + v.n + 1) - end;
+    all = __ldg(v.header + 2 + v.list) - (none + 63) / 64;
+    lo = (int)((int64_t)all * rank / C);
+    hi = (int)((int64_t)all * (rank + 1) / C);
+  }
+  // desc[i] = tile w0 - 1 + i (position, adapter) for the window's tiles and one on either side;
+  // before the first: adapter -1; after the last: `end`, adapter -1. Needs blockDim >= kWindow + 2.
+  __device__ __forceinline__ void window(const PlanView& v, int w0, int2* desc) const {
+    const int k = w0 - 1 + (int)threadIdx.x;
+    if (threadIdx.x < kWindow + 2)
+      desc[threadIdx.x] = (k >= 0 && k < all) ? __ldg(v.tiles + k) : make_int2(k < 0 ? 0 : end, -1);
+  }
+};
+
 // Cluster of this CTA (one-dimensional).
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned v;
@@ -105,6 +129,12 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, unsigned rank) {
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ld_cluster_f1(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
 

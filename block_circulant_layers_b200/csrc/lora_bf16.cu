@@ -1,18 +1,22 @@
-// Low-rank adapters of many requests, bf16: rows kernel (forward, grad_x) and weight
+// Low-rank adapters of many requests, bf16: rows kernels (forward, grad_x) and weight
 // gradients. fp32 accumulation throughout.
 //
-// A tile of the plan is up to M tokens of one adapter. One cluster of CTAs computes it in one
-// launch: each CTA multiplies its share of the K columns of the tile's rows with its share of
-// w1 (mid = in w1^T, r columns), the partial sums are added over the cluster through
+// A tile of the plan is up to 16 or 64 tokens of one adapter. One cluster of CTAs computes it
+// in one launch: each CTA multiplies its share of the K columns of the tile's rows with its
+// share of w1 (mid = in w1^T, r columns), the partial sums are added over the cluster through
 // distributed shared memory in rank order, and each CTA then expands mid to its share of the N
 // output columns (out = base + scale mid w2^T). So every row is read once and written once,
 // and A and B once per tile; the sums do not depend on timing.
 //
-// The products run on mma.m16n8k16 with operand fragments loaded straight from global memory:
-// the contraction index may be taken in any order as long as both operands agree, so a lane
-// takes 16 consecutive bytes of a row where the instruction's layout would scatter them. With
-// r <= 128 the work is 2 r flops per byte of a row at most, and the rows, not the tensor
-// pipe, set the time; tensor memory would only add a trip for a result of r columns.
+// The products run on mma.m16n8k16. With r <= 128 the work is 2 r flops per byte of a row at
+// most, and the rows, not the tensor pipe, set the time; tensor memory would only add a trip
+// for a result of r columns.
+//  * k_lora_rows16 (decode, small groups): operand fragments straight from global memory. The
+//    contraction index may be taken in any order as long as both operands agree, so a lane
+//    takes 16 consecutive bytes of a row where the instruction's layout would scatter them.
+//    No staging and one barrier before the cluster's: few tokens are a matter of latency.
+//  * k_lora_rows64: steps of 64 or 128 columns of rows and weights through a ring of cp.async stages, the
+//    second half's steps (base, w2) requested while the cluster adds up the first half's.
 #include "lora.cuh"
 
 #include "many_policy.h"
@@ -71,18 +75,15 @@ __device__ __forceinline__ float hi_f32(uint32_t v) { return __uint_as_float(v &
 template <int R>
 constexpr int mid_stride() { return R == 16 ? 16 : R + 16; }
 
-template <int R, int M>
-constexpr size_t rows_smem() {
-  constexpr int MT = M == 16 ? 1 : (R <= 32 ? 4 : 128 / R);
-  constexpr int WK = kWarps / (M / (16 * MT));
-  return sizeof(float) * WK * M * R + 2 * sizeof(bf16_t) * M * mid_stride<R>();
+template <int R>
+constexpr size_t rows16_smem() {
+  return sizeof(float) * kWarps * 16 * R + 2 * sizeof(bf16_t) * 16 * mid_stride<R>();
 }
 
-// R: r rounded up to 16, 32, 64 or 128. M: tokens per tile, 16 or 64 (the plan's list).
-template <int R, int M, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
-  constexpr int MT = M == 16 ? 1 : (R <= 32 ? 4 : 128 / R);   // 16-row tiles per warp: 64 accumulators at most
-  constexpr int WM = M / (16 * MT), WK = kWarps / WM;          // row groups x shares of K
+// R: r rounded up to 16, 32, 64 or 128.
+template <int R, bool BWD>
+__global__ void __launch_bounds__(kThreads) k_lora_rows16(LoraRows<bf16_t> a) {
+  constexpr int M = 16, WK = kWarps;                           // the warps share the K columns
   constexpr int NJ = R / 8;
   constexpr int V = R / 8;                                     // r values per lane of a w1 row, backward
   constexpr int MS = mid_stride<R>();
@@ -102,49 +103,54 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
   const int K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
 
+  // the output's rows, columns and first base values: requested early, used in the second half
+  const int groups = (N + 63) / 64;
+  const int gr0 = (int)((int64_t)groups * rank / C) + warp, g1 = (int)((int64_t)groups * (rank + 1) / C);
+  int tok[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) tok[h] = g + 8 * h < m ? __ldg(a.plan.order + pos0 + g + 8 * h) : -1;
+  // a lane holds two runs of 8 columns of each of its rows: 8 (2 q + run) + [0, 8)
+  uint4 next[2][2];
+  auto load_base = [&](int gr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int run = 0; run < 2; ++run) {
+        const int c = 64 * gr + 16 * q + 8 * run;
+        next[h][run] = make_uint4(0, 0, 0, 0);
+        if (a.base && tok[h] >= 0 && c < N)
+          next[h][run] = *reinterpret_cast<const uint4*>(a.base + (int64_t)tok[h] * N + c);
+      }
+  };
+
   if (adapted) {
     // ---- mid = in w1^T over this CTA's units of 32 columns
-    const int wm = warp % WM, wk = warp / WM;
     const int units = (K + 31) / 32;
     const int u0 = (int)((int64_t)units * rank / C), u1 = (int)((int64_t)units * (rank + 1) / C);
-    const bf16_t* row[MT][2];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = (wm * MT + i) * 16 + g + 8 * h;
-        row[i][h] = t < m ? a.in + (int64_t)__ldg(a.plan.order + pos0 + t) * K : nullptr;
-      }
+    const bf16_t* const row0 = a.in + (int64_t)tok[0] * K;
+    const bf16_t* const row1 = a.in + (int64_t)tok[1] * K;
     const bf16_t* const w1 = a.w1 + (int64_t)ad * r * K;
-    float acc[MT][NJ][4];
+    float acc[NJ][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
 
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 2
-    for (int u = u0 + wk; u < u1; u += WK) {
+    for (int u = u0 + warp; u < u1; u += WK) {
       const int k0 = 32 * u + 8 * q;                           // this lane's 8 columns
       const bool in = k0 < K;
-      uint4 xa[MT][2];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) xa[i][h] = (in && row[i][h]) ? ldg16(row[i][h] + k0) : zero;
+      const uint4 x0 = (in && tok[0] >= 0) ? ldg16(row0 + k0) : zero;
+      const uint4 x1 = (in && tok[1] >= 0) ? ldg16(row1 + k0) : zero;
       if constexpr (!BWD) {
         // w1 row 8 j + g, the same 8 columns
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const int rho = 8 * j + g;
           const uint4 wb = (in && rho < r) ? ldg16(w1 + (int64_t)rho * K + k0) : zero;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma16816(acc[i][j], xa[i][0].x, xa[i][1].x, xa[i][0].y, xa[i][1].y, wb.x, wb.y);
-            mma16816(acc[i][j], xa[i][0].z, xa[i][1].z, xa[i][0].w, xa[i][1].w, wb.z, wb.w);
-          }
+          mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, wb.x, wb.y);
+          mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, wb.z, wb.w);
         }
       } else {
         // w1 is read where B lies: column k0 + e of w1 is row k0 + e of B, r values of which
@@ -169,26 +175,21 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
           }
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma16816(acc[i][j], xa[i][0].x, xa[i][1].x, xa[i][0].y, xa[i][1].y, pair_of(wr[0], wr[1], j),
-                     pair_of(wr[2], wr[3], j));
-            mma16816(acc[i][j], xa[i][0].z, xa[i][1].z, xa[i][0].w, xa[i][1].w, pair_of(wr[4], wr[5], j),
-                     pair_of(wr[6], wr[7], j));
-          }
+        for (int j = 0; j < NJ; ++j) {
+          mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, pair_of(wr[0], wr[1], j), pair_of(wr[2], wr[3], j));
+          mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, pair_of(wr[4], wr[5], j), pair_of(wr[6], wr[7], j));
+        }
       }
     }
+    if (gr0 < g1) load_base(gr0);
     // the column of tile j that a lane holds is 2 q + e
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = (wm * MT + i) * 16 + g + 8 * (e / 2), c = 2 * q + (e & 1);
-          part[(wk * M + t) * R + (BWD ? V * c + j : 8 * j + c)] = acc[i][j][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int t = g + 8 * (e / 2), c = 2 * q + (e & 1);
+        part[(warp * M + t) * R + (BWD ? V * c + j : 8 * j + c)] = acc[j][e];
+      }
     __syncthreads();
     // this CTA's sum, in place of the first share
     for (int e = 4 * threadIdx.x; e < M * R; e += 4 * kThreads) {
@@ -234,9 +235,9 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
     }
     if (C > 1) cluster_arrive();                               // done with the others' memory
     __syncthreads();
-  } else if (a.mid) {
-    // tokens without an adapter: mid is zero
-    for (int e = threadIdx.x; e < m * r; e += kThreads) {
+  } else {
+    if (gr0 < g1) load_base(gr0);
+    for (int e = threadIdx.x; a.mid != nullptr && e < m * r; e += kThreads) {   // mid is zero
       const int t = e / r;
       if ((unsigned)(t % C) == rank) a.mid[(int64_t)__ldg(a.plan.order + pos0 + t) * r + e % r] = 0.0f;
     }
@@ -245,42 +246,20 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
 
   // ---- out = base + mid w2^T over this CTA's groups of 64 columns
   if (a.out != nullptr && (adapted || a.base != a.out)) {
-    constexpr int MT2 = M == 16 ? 1 : 2;
-    constexpr int RG = M / (16 * MT2);                         // row groups; the other warps take columns
-    const int rg = warp % RG, cw = warp / RG;
-    const int groups = (N + 63) / 64;
-    const int g0 = (int)((int64_t)groups * rank / C), g1 = (int)((int64_t)groups * (rank + 1) / C);
     const bf16_t* const w2 = a.w2 + (int64_t)(adapted ? ad : 0) * r * N;
-    int64_t orow[MT2][2];
-#pragma unroll
-    for (int i = 0; i < MT2; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = (rg * MT2 + i) * 16 + g + 8 * h;
-        orow[i][h] = t < m ? (int64_t)__ldg(a.plan.order + pos0 + t) * N : -1;
-      }
-    for (int gr = g0 + cw; gr < g1; gr += kWarps / RG) {
+    for (int gr = gr0; gr < g1; gr += kWarps) {
       const int n0 = 64 * gr;
-      // a lane ends with two runs of 8 columns of each of its rows: 8 (2 q + run) + [0, 8)
-      uint4 bs[MT2][2][2];
+      uint4 bs[2][2];
 #pragma unroll
-      for (int i = 0; i < MT2; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int run = 0; run < 2; ++run) bs[h][run] = next[h][run];
+      if (gr + kWarps < g1) load_base(gr + kWarps);
+      float acc[8][4];
 #pragma unroll
-          for (int run = 0; run < 2; ++run) {
-            const int c = n0 + 16 * q + 8 * run;
-            bs[i][h][run] = make_uint4(0, 0, 0, 0);
-            if (a.base && orow[i][h] >= 0 && c < N)
-              bs[i][h][run] = *reinterpret_cast<const uint4*>(a.base + orow[i][h] + c);
-          }
-      float acc[MT2][8][4];
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int i = 0; i < MT2; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
       if (adapted) {
         const int col = n0 + 8 * g;                            // tile j's column g is output column col + j
 #pragma unroll
@@ -305,145 +284,498 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(LoraRows<bf16_t> a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) b0[j] = pair_of(wr[0], wr[1], j), b1[j] = pair_of(wr[2], wr[3], j);
           }
+          const uint2 h0 = *reinterpret_cast<const uint2*>(mid_hi + g * MS + rho);
+          const uint2 h1 = *reinterpret_cast<const uint2*>(mid_hi + (g + 8) * MS + rho);
+          const uint2 l0 = *reinterpret_cast<const uint2*>(mid_lo + g * MS + rho);
+          const uint2 l1 = *reinterpret_cast<const uint2*>(mid_lo + (g + 8) * MS + rho);
 #pragma unroll
-          for (int i = 0; i < MT2; ++i) {
-            const int t = (rg * MT2 + i) * 16 + g;
-            const uint2 h0 = *reinterpret_cast<const uint2*>(mid_hi + t * MS + rho);
-            const uint2 h1 = *reinterpret_cast<const uint2*>(mid_hi + (t + 8) * MS + rho);
-            const uint2 l0 = *reinterpret_cast<const uint2*>(mid_lo + t * MS + rho);
-            const uint2 l1 = *reinterpret_cast<const uint2*>(mid_lo + (t + 8) * MS + rho);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              mma16816(acc[i][j], h0.x, h1.x, h0.y, h1.y, b0[j], b1[j]);
-              mma16816(acc[i][j], l0.x, l1.x, l0.y, l1.y, b0[j], b1[j]);
-            }
+          for (int j = 0; j < 8; ++j) {
+            mma16816(acc[j], h0.x, h1.x, h0.y, h1.y, b0[j], b1[j]);
+            mma16816(acc[j], l0.x, l1.x, l0.y, l1.y, b0[j], b1[j]);
           }
         }
       }
 #pragma unroll
-      for (int i = 0; i < MT2; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int run = 0; run < 2; ++run) {
+          const int c = n0 + 16 * q + 8 * run;
+          if (tok[h] < 0 || c >= N) continue;
+          const uint32_t b[4] = {bs[h][run].x, bs[h][run].y, bs[h][run].z, bs[h][run].w};
+          uint32_t o[4];
 #pragma unroll
-          for (int run = 0; run < 2; ++run) {
-            const int c = n0 + 16 * q + 8 * run;
-            if (orow[i][h] < 0 || c >= N) continue;
-            const uint32_t b[4] = {bs[i][h][run].x, bs[i][h][run].y, bs[i][h][run].z, bs[i][h][run].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              o[x] = pack2(acc[i][2 * x][2 * h + run] + lo_f32(b[x]), acc[i][2 * x + 1][2 * h + run] + hi_f32(b[x]));
-            *reinterpret_cast<uint4*>(a.out + orow[i][h] + c) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          for (int x = 0; x < 4; ++x)
+            o[x] = pack2(acc[2 * x][2 * h + run] + lo_f32(b[x]), acc[2 * x + 1][2 * h + run] + hi_f32(b[x]));
+          *reinterpret_cast<uint4*>(a.out + (int64_t)tok[h] * N + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
   }
   if (adapted && C > 1) cluster_wait();                        // the others are done with this CTA's memory
 }
 
-// ------------------------------------------------------------------- weight gradients
-// One CTA: 64 columns of x (grad_a) or of g (grad_b) over all tokens of one adapter. D[rho,
-// column] = sum_t mid[t, rho] row[t, column]: tokens are the contraction index, so the rows'
-// fragments are pairs of tokens, built from 16-byte pieces of four rows. The 8 warps share
-// the tokens (and, from r > 32 on, the rho range) and add their sums in a fixed order.
-// mid is fp32; it enters the product as three bf16 summing to it exactly in all but the last
-// bits (24 mantissa bits), since the gradients are fp32.
+// ------------------------------------------------------------- staging and fragments
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory; zeros when !in (src is then not read, but must be a valid pointer).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
+
+// Byte offset of 16-byte unit `unit` of row `row` in a tile of W bf16 columns. The units of a
+// row are permuted by the row so that 8 rows' units of one column fall into different banks.
+template <int W>
+__device__ __forceinline__ uint32_t at(int row, int unit) {
+  const int f = W == 16 ? (row >> 2) & 1 : (W == 32 ? (row >> 1) & 3 : row & 7);
+  return row * 2 * W + 16 * (unit ^ f);
+}
+
+// Fragments from a tile of W columns at `base`. Operand rows (tokens, or output columns) by
+// contraction index, 16 of each at (row0, k0), lie in the tile as they are (n: not transposed)
+// or with the contraction index as the row (t). An A fragment is one of them; for B, x4 gives
+// {b0, b1} of rows row0..+7 and of row0 + 8..+15.
+template <int W>
+__device__ __forceinline__ void frag_a_n(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
+  ldsm4(v, base + at<W>(row0 + (lane / 8 & 1) * 8 + lane % 8, k0 / 8 + lane / 16));
+}
+template <int W>
+__device__ __forceinline__ void frag_a_t(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
+  ldsm4t(v, base + at<W>(k0 + lane / 16 * 8 + lane % 8, row0 / 8 + (lane / 8 & 1)));
+}
+template <int W>
+__device__ __forceinline__ void frag_b_n(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
+  ldsm4(v, base + at<W>(row0 + lane / 16 * 8 + lane % 8, k0 / 8 + (lane / 8 & 1)));
+}
+template <int W>
+__device__ __forceinline__ void frag_b_t(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
+  ldsm4t(v, base + at<W>(k0 + (lane / 8 & 1) * 8 + lane % 8, row0 / 8 + lane / 16));
+}
+
+// ----------------------------------------------------------------- rows, 64-token tiles
 template <int R>
-__global__ void __launch_bounds__(kThreads) k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
-  constexpr int MT = R == 16 ? 1 : 2;                          // 16-row tiles of rho per warp
-  constexpr int WR = R / (16 * MT), WT = kWarps / WR;          // rho groups x shares of the tokens
-  extern __shared__ __align__(16) float part[];                // [WT][R][64]
+struct Rows64 {
+  static constexpr int kCols = R <= 32 ? 128 : 64;           // columns per step
+  static constexpr int kRowBytes = 64 * kCols * 2;           // 64 rows of in or base
+  static constexpr int kStage = kRowBytes + kCols * R * 2;   // and those columns of w1 or w2
+  static constexpr int kStages = R == 64 ? 4 : 3;
+  static constexpr size_t smem = (size_t)kStage * kStages + sizeof(float) * 2 * 64 * R + 2 * 64 * R * sizeof(bf16_t);
+};
+
+template <int R, bool BWD>
+__global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a) {
+  using S = Rows64<R>;
+  constexpr int M = 64, COLS = S::kCols, UNITS = COLS / 8, ROWS = kThreads / UNITS, NH = M / ROWS;
+  extern __shared__ __align__(128) unsigned char ring[];
+  float* const part = reinterpret_cast<float*>(ring + S::kStage * S::kStages);     // [2][M][R]
+  const uint32_t ring_at = smem_addr(ring);
+  const uint32_t hi_at = smem_addr(part + 2 * M * R), lo_at = hi_at + M * R * 2;   // mid, tiles of R columns
+  unsigned char* const mid_hi = reinterpret_cast<unsigned char*>(part + 2 * M * R);
+  unsigned char* const mid_lo = mid_hi + M * R * 2;
+
   griddep_wait();
   if (!plan_matches(a.plan)) return;
-  const int ad = blockIdx.y, r = a.r;
-  const bool is_a = (int)blockIdx.x < blocks_a;
-  const int n0 = 64 * (is_a ? blockIdx.x : blockIdx.x - blocks_a);
+  const unsigned C = cluster_size(), rank = cluster_rank();
+  const int tile = blockIdx.x / C;
+  const int2 te = __ldg(a.plan.tiles + tile);                  // within the list's capacity
+  if (tile >= __ldg(a.plan.header + 2 + a.plan.list)) return;  // the whole cluster leaves
+  const int pos0 = te.x, ad = te.y;
+  const int m = min(__ldg(a.plan.offsets + ad + 1) - pos0, M);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
+  const int K = a.K, N = a.N, r = a.r;
+  const bool adapted = ad < a.plan.n;
+
+  // this CTA's steps of COLS columns: [0, n1) of in and w1, then [n1, n1 + n2) of base and w2
+  const int ks = (K + COLS - 1) / COLS, ns = (N + COLS - 1) / COLS;
+  const int k_first = (int)((int64_t)ks * rank / C), n_first = (int)((int64_t)ns * rank / C);
+  const int n1 = adapted ? (int)((int64_t)ks * (rank + 1) / C) - k_first : 0;
+  const int n2 = (a.out != nullptr && (adapted || a.base != a.out)) ? (int)((int64_t)ns * (rank + 1) / C) - n_first : 0;
+  const bf16_t* const w1 = a.w1 + (adapted ? (int64_t)ad * r * K : 0);
+  const bf16_t* const w2 = a.w2 + (adapted ? (int64_t)ad * r * N : 0);
+  // a thread moves one unit of every ROWS-th row of a row tile
+  const int trow = tid / UNITS, tunit = tid % UNITS;
+  int tok[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) tok[h] = trow + ROWS * h < m ? __ldg(a.plan.order + pos0 + trow + ROWS * h) : -1;
+
+  auto request = [&](int step) {
+    if (step < n1 + n2) {
+      const bool first = step < n1;
+      const int c0 = COLS * (first ? k_first + step : n_first + step - n1), W = first ? K : N;
+      const bf16_t* const rows = first ? a.in : a.base;
+      const uint32_t dst = ring_at + step % S::kStages * S::kStage;
+      const int c = c0 + 8 * tunit;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const bool in = rows != nullptr && tok[h] >= 0 && c < W;
+        cp16(dst + at<COLS>(trow + ROWS * h, tunit), in ? rows + (int64_t)tok[h] * W + c : a.in, in);
+      }
+      if (adapted) {
+        const bf16_t* const w = first ? w1 : w2;
+        const uint32_t wdst = dst + S::kRowBytes;
+        // r rows of COLS columns (w1 forward, w2 backward), or COLS rows of r columns
+        const bool along = first != BWD;
+#pragma unroll
+        for (int i = 0; i < (UNITS * R + kThreads - 1) / kThreads; ++i) {
+          const int e = tid + kThreads * i;
+          if (UNITS * R < kThreads && e >= UNITS * R) break;
+          if (along) {
+            const int rho = e / UNITS, cc = c0 + e % UNITS * 8;
+            const bool in = rho < r && cc < W;
+            cp16(wdst + at<COLS>(rho, e % UNITS), in ? w + (int64_t)rho * W + cc : w, in);
+          } else {
+            const int cr = e / (R / 8), u = e % (R / 8);
+            const bool in = c0 + cr < W && 8 * u < r;
+            cp16(wdst + at<R>(cr, u), in ? w + (int64_t)(c0 + cr) * r + 8 * u : w, in);
+          }
+        }
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) request(s);
+
+  const int wm = warp % 4, wh = warp / 4;                      // 16 rows; half of a step's columns
+  if (adapted) {
+    float acc[R / 8][4];
+#pragma unroll
+    for (int j = 0; j < R / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+    for (int step = 0; step < n1; ++step) {
+      cp_wait<S::kStages - 2>();
+      __syncthreads();
+      request(step + S::kStages - 1);
+      const uint32_t x_at = ring_at + step % S::kStages * S::kStage, w_at = x_at + S::kRowBytes;
+#pragma unroll
+      for (int k = COLS / 2 * wh; k < COLS / 2 * (wh + 1); k += 16) {
+        uint32_t x[4];
+        frag_a_n<COLS>(x, x_at, 16 * wm, k, lane);
+#pragma unroll
+        for (int j = 0; j < R / 16; ++j) {
+          uint32_t w[4];
+          if constexpr (!BWD) frag_b_n<COLS>(w, w_at, 16 * j, k, lane);
+          else frag_b_t<R>(w, w_at, 16 * j, k, lane);
+          mma16816(acc[2 * j], x[0], x[1], x[2], x[3], w[0], w[1]);
+          mma16816(acc[2 * j + 1], x[0], x[1], x[2], x[3], w[2], w[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R / 8; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(part + (wh * M + 16 * wm + g + 8 * h) * R + 8 * j + 2 * q) =
+            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+    __syncthreads();
+    // this CTA's sum, in place of the first half's
+    for (int e = 4 * tid; e < M * R; e += 4 * kThreads) {
+      float4 s = *reinterpret_cast<float4*>(part + e);
+      const float4 v = *reinterpret_cast<const float4*>(part + M * R + e);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      *reinterpret_cast<float4*>(part + e) = s;
+    }
+    if (C > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    // the cluster's sum in rank order, every CTA for itself; mid is scaled and kept as the sum
+    // of two bf16, hi + lo (16 mantissa bits), so its rounding stays far below the output's
+    const float scale = a.scale ? __ldg(a.scale + ad) : 1.0f;
+    for (int e = 4 * tid; e < M * R; e += 4 * kThreads) {
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (C > 1) {
+        for (unsigned c = 0; c < C; ++c) {
+          const float4 v = ld_cluster_f4(map_rank(part + e, c));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+      } else {
+        s = *reinterpret_cast<const float4*>(part + e);
+      }
+      const int t = e / R, c = e % R;
+      // columns beyond r stay zero even where a row holds an infinity (0 x inf)
+      const float4 ss = c < r ? make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (a.mid && t < m && c < r && (unsigned)(t % C) == rank)
+        *reinterpret_cast<float4*>(a.mid + (int64_t)__ldg(a.plan.order + pos0 + t) * r + c) = BWD ? ss : s;
+      const uint32_t h0 = pack2(ss.x, ss.y), h1 = pack2(ss.z, ss.w);
+      const uint32_t o = at<R>(t, c / 8) + (c & 4) * 2;
+      *reinterpret_cast<uint2*>(mid_hi + o) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(mid_lo + o) =
+          make_uint2(pack2(ss.x - lo_f32(h0), ss.y - hi_f32(h0)), pack2(ss.z - lo_f32(h1), ss.w - hi_f32(h1)));
+    }
+    if (C > 1) cluster_arrive();                               // done with the others' memory
+  } else if (a.mid != nullptr) {
+    for (int e = tid; e < m * r; e += kThreads) {              // mid is zero
+      const int t = e / r;
+      if ((unsigned)(t % C) == rank) a.mid[(int64_t)__ldg(a.plan.order + pos0 + t) * r + e % r] = 0.0f;
+    }
+  }
+  griddep_launch_dependents();
+
+  for (int step = n1; step < n1 + n2; ++step) {
+    cp_wait<S::kStages - 2>();
+    __syncthreads();                                           // the stage, and at first mid, is complete
+    request(step + S::kStages - 1);
+    unsigned char* const tile_p = ring + step % S::kStages * S::kStage;
+    const uint32_t w_at = ring_at + step % S::kStages * S::kStage + S::kRowBytes;
+    if (adapted) {
+      float acc[COLS / 16][4];
+#pragma unroll
+      for (int j = 0; j < COLS / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < R; k += 16) {
+        uint32_t h[4], l[4];
+        frag_a_n<R>(h, hi_at, 16 * wm, k, lane);
+        frag_a_n<R>(l, lo_at, 16 * wm, k, lane);
+#pragma unroll
+        for (int j = 0; j < COLS / 32; ++j) {
+          uint32_t w[4];
+          if constexpr (!BWD) frag_b_n<R>(w, w_at, COLS / 2 * wh + 16 * j, k, lane);
+          else frag_b_t<COLS>(w, w_at, COLS / 2 * wh + 16 * j, k, lane);
+          mma16816(acc[2 * j], h[0], h[1], h[2], h[3], w[0], w[1]);
+          mma16816(acc[2 * j + 1], h[0], h[1], h[2], h[3], w[2], w[3]);
+          mma16816(acc[2 * j], l[0], l[1], l[2], l[3], w[0], w[1]);
+          mma16816(acc[2 * j + 1], l[0], l[1], l[2], l[3], w[2], w[3]);
+        }
+      }
+      // the sum with base replaces it in the stage (zeros where there is none)
+#pragma unroll
+      for (int j = 0; j < COLS / 16; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(tile_p + at<COLS>(16 * wm + g + 8 * h, UNITS / 2 * wh + j) + 4 * q);
+          *p = pack2(acc[j][2 * h] + lo_f32(*p), acc[j][2 * h + 1] + hi_f32(*p));
+        }
+      __syncthreads();
+    }
+    const int c = COLS * (n_first + step - n1) + 8 * tunit;
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+      if (tok[h] >= 0 && c < N)
+        *reinterpret_cast<uint4*>(a.out + (int64_t)tok[h] * N + c) =
+            *reinterpret_cast<const uint4*>(tile_p + at<COLS>(trow + ROWS * h, tunit));
+  }
+  cp_wait<0>();
+  if (adapted && C > 1) cluster_wait();                        // the others are done with this CTA's memory
+}
+
+// ------------------------------------------------------------------- weight gradients
+// One cluster: 128 (64 at r > 64) columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
+// plan's 64-token tiles evenly (TileShare). D[rho, column] = sum_t mid[t, rho] row[t, column]:
+// tokens are the contraction index, and both operands are read transposed. A warp has 16
+// columns and every rho (half of them at r > 64), so no sums are shared inside a CTA. An adapter whose tiles lie in
+// several CTAs is written by the first of them, which adds the others' sums in rank order
+// through distributed shared memory.
+// Tiles pass through a ring of cp.async stages: a tile's token numbers are requested four
+// steps ahead, its rows two steps ahead.
+// mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits
+// (24 mantissa bits), since the gradients are fp32.
+template <int R>
+struct Wgrad {
+  static constexpr int kCols = R <= 64 ? 128 : 64, kTok = 64, kStages = 3, kOrders = 8;
+  static constexpr int kWC = kCols / 16, kNI = R / 16 / (kWarps / kWC);   // column groups; rho tiles per warp
+  static constexpr int kRowBytes = kTok * kCols * 2;
+  static constexpr int kStage = kRowBytes + kTok * R * 4;     // rows, and mid in fp32
+  static constexpr int kMid = 3 * kTok * R * 2;               // mid as three tiles of R columns
+  static constexpr int kHead = R * kCols * 4;
+  static constexpr size_t smem = (size_t)kStage * kStages + kMid + kHead;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, R == 16 ? 3 : (R == 32 ? 2 : 1))
+k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
+  using S = Wgrad<R>;
+  constexpr int COLS = S::kCols, UNITS = COLS / 8, NI = S::kNI;
+  constexpr int NA = NI * 8;                                   // sums per thread
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ int2 desc[kWindow + 2];
+  __shared__ __align__(16) int order[S::kOrders][S::kTok];
+  unsigned char* const mid_p = ring + S::kStage * S::kStages;
+  float* const head = reinterpret_cast<float*>(mid_p + S::kMid);   // [NA][kThreads]
+  const uint32_t ring_at = smem_addr(ring), mid_at = smem_addr(mid_p);
+  griddep_wait();
+  if (!plan_matches(a.plan)) return;
+  const unsigned C = cluster_size(), rank = cluster_rank();
+  const int r = a.r, block = blockIdx.x / C;
+  const bool is_a = block < blocks_a;
+  const int n0 = S::kCols * (is_a ? block : block - blocks_a);
   const int W = is_a ? a.K : a.N;                              // columns of the rows read
   const bf16_t* const rows = is_a ? a.x : a.g;
   const float* const mid = is_a ? a.v : a.u;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int wr = warp % WR, wt = warp / WR;
-  const int beg = __ldg(a.plan.offsets + ad), end = __ldg(a.plan.offsets + ad + 1);
-  const int col = n0 + 8 * g;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
+  const int wc = warp % S::kWC, rho0 = 16 * NI * (warp / S::kWC);
+  const TileShare share(a.plan, rank, C);
 
-  float acc[MT][8][4];
+  float acc[NA];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < NA; ++e) acc[e] = 0.0f;
+  };
+  // sums of adapter ad to global memory; acc[8 i + 4 j + 2 h + e] is row rho0 + 16 i + g + 8 h,
+  // column 16 wc + 8 j + 2 q + e
+  auto write = [&](int ad) {
+    const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-#pragma unroll 2
-  for (int p0 = beg + 16 * wt; p0 < end; p0 += 16 * WT) {
-    int64_t tok[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int pos = p0 + 4 * q + e;
-      tok[e] = pos < end ? __ldg(a.plan.order + pos) : -1;
-    }
-    uint32_t w[4][4];
-    float mv[MT][2][4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) w[e][x] = 0;
-      if (tok[e] >= 0 && col < W) ldg_words<4>(rows + tok[e] * W + col, w[e]);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int rho = (wr * MT + i) * 16 + g + 8 * h;
-          mv[i][h][e] = (tok[e] >= 0 && rho < r) ? __ldg(mid + tok[e] * r + rho) : 0.0f;
-        }
-    }
-    uint32_t b0[8], b1[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b0[j] = pair_of(w[0], w[1], j), b1[j] = pair_of(w[2], w[3], j);
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        uint32_t f[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float &v0 = mv[i][h][2 * x], &v1 = mv[i][h][2 * x + 1];
-            f[h][x] = pack2(v0, v1);
-            v0 -= lo_f32(f[h][x]);
-            v1 -= hi_f32(f[h][x]);
+          const int rho = rho0 + 16 * i + g + 8 * h, c = n0 + 16 * wc + 8 * j + 2 * q;
+          if (rho >= r || c >= W) continue;
+          const float* v = acc + 8 * i + 4 * j + 2 * h;
+          if (is_a) {
+            *reinterpret_cast<float2*>(a.grad_a + ((int64_t)ad * r + rho) * W + c) = make_float2(v[0], v[1]);
+          } else {
+            float* dst = a.grad_b + ((int64_t)ad * W + c) * r + rho;
+            dst[0] = scale * v[0];
+            dst[r] = scale * v[1];
           }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mma16816(acc[i][j], f[0][0], f[1][0], f[0][1], f[1][1], b0[j], b1[j]);
+        }
+  };
+
+  clear();
+  int open = -1;                                               // adapter whose sums go on in the next CTA
+  bool from_before = false;                                    // the sum at hand began in an earlier CTA
+  for (int w0 = share.lo; w0 < share.hi; w0 += kWindow) {
+    const int count = min(kWindow, share.hi - w0);
+    __syncthreads();                                           // the last window is consumed
+    share.window(a.plan, w0, desc);
+    __syncthreads();
+    auto request_order = [&](int i) {
+      if (i < count && tid < S::kTok) {
+        const int pos = desc[i + 1].x + tid;
+        const bool in = pos < desc[i + 2].x;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(&order[i % S::kOrders][tid])),
+                     "l"(in ? a.plan.order + pos : a.plan.order), "r"(in ? 4 : 0)
+                     : "memory");
       }
+    };
+    auto request = [&](int i) {
+      if (i < count) {
+        const int tokens = desc[i + 2].x - desc[i + 1].x;
+        const int* const ord = order[i % S::kOrders];
+        const uint32_t dst = ring_at + i % S::kStages * S::kStage;
+#pragma unroll
+        for (int h = 0; h < S::kTok * UNITS / kThreads; ++h) {
+          const int t = tid / UNITS + kThreads / UNITS * h, c = n0 + tid % UNITS * 8;
+          const bool in = t < tokens && c < W;
+          cp16(dst + at<COLS>(t, tid % UNITS), in ? rows + (int64_t)ord[t] * W + c : rows, in);
+        }
+#pragma unroll
+        for (int h = 0; h < R / 16; ++h) {
+          const int e = tid + kThreads * h, t = e / (R / 4), c = e % (R / 4) * 4;
+          const bool in = t < tokens && c < r;
+          cp16(dst + S::kRowBytes + (t * R + c) * 4, in ? mid + (int64_t)ord[t] * r + c : mid, in);
+        }
+      }
+    };
+    request_order(0);
+    request_order(1);
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    request(0);
+    request_order(2);
+    cp_commit();
+    request(1);
+    request_order(3);
+    cp_commit();
+    if (w0 == share.lo) from_before = desc[0].y == desc[1].y;
+    for (int i = 0; i < count; ++i) {
+      cp_wait<1>();                                            // all but the last request: rows i, order i + 2
+      __syncthreads();
+      request(i + 2);
+      request_order(i + 4);
+      cp_commit();
+      const unsigned char* const stage = ring + i % S::kStages * S::kStage;
+#pragma unroll
+      for (int h = 0; h < R / 16; ++h) {
+        const int e = tid + kThreads * h, t = e / (R / 4), c = e % (R / 4) * 4;
+        float4 v = *reinterpret_cast<const float4*>(stage + S::kRowBytes + (t * R + c) * 4);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+          const uint32_t p0 = pack2(v.x, v.y), p1 = pack2(v.z, v.w);
+          *reinterpret_cast<uint2*>(mid_p + s * S::kTok * R * 2 + at<R>(t, c / 8) + (c & 4) * 2) = make_uint2(p0, p1);
+          v.x -= lo_f32(p0), v.y -= hi_f32(p0), v.z -= lo_f32(p1), v.w -= hi_f32(p1);
+        }
+      }
+      __syncthreads();
+      const uint32_t x_at = ring_at + i % S::kStages * S::kStage;
+      const int tokens = desc[i + 2].x - desc[i + 1].x, ad = desc[i + 1].y;
+#pragma unroll
+      for (int k = 0; k < S::kTok; k += 16) {
+        if (k >= tokens) break;
+        uint32_t b[4];
+        frag_b_t<COLS>(b, x_at, 16 * wc, k, lane);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          float(&d0)[4] = *reinterpret_cast<float(*)[4]>(acc + 8 * j);
+          float(&d1)[4] = *reinterpret_cast<float(*)[4]>(acc + 8 * j + 4);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {
+            uint32_t f[4];
+            frag_a_t<R>(f, mid_at + s * S::kTok * R * 2, rho0 + 16 * j, k, lane);
+            mma16816(d0, f[0], f[1], f[2], f[3], b[0], b[1]);
+            mma16816(d1, f[0], f[1], f[2], f[3], b[2], b[3]);
+          }
+        }
+      }
+      const bool goes_on = desc[i + 2].y == ad;                // the next tile is the same adapter's
+      if (w0 + i + 1 == share.hi && goes_on && !from_before) {
+        open = ad;                                             // its sums stay here
+      } else if (!goes_on || w0 + i + 1 == share.hi) {
+        if (from_before) {                                     // an earlier CTA writes it
+#pragma unroll
+          for (int e = 0; e < NA; ++e) head[e * kThreads + tid] = acc[e];
+          from_before = false;
+        } else {
+          write(ad);
+        }
+        clear();
+      }
+    }
+    cp_wait<0>();
   }
   griddep_launch_dependents();
-  // [rho][column] sums of each share, then their sum; column 8 (2 q + e) + j of the group
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (open >= 0) {
+      // the CTAs after this one up to the adapter's end hold its other sums
+      for (unsigned k = rank + 1; k < C; ++k) {
+        const int klo = (int)((int64_t)share.all * k / C), khi = (int)((int64_t)share.all * (k + 1) / C);
+        if (klo == khi) continue;                              // no tiles there
+        if (__ldg(a.plan.tiles + klo).y != open) break;
+        const uint32_t src = map_rank(head, k);
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* dst = part + ((wt * R + (wr * MT + i) * 16 + g + 8 * h) * 64 + 16 * q + 8 * e);
-        *reinterpret_cast<float4*>(dst) =
-            make_float4(acc[i][0][2 * h + e], acc[i][1][2 * h + e], acc[i][2][2 * h + e], acc[i][3][2 * h + e]);
-        *reinterpret_cast<float4*>(dst + 4) =
-            make_float4(acc[i][4][2 * h + e], acc[i][5][2 * h + e], acc[i][6][2 * h + e], acc[i][7][2 * h + e]);
+        for (int e = 0; e < NA; ++e) acc[e] += ld_cluster_f1(src + 4 * (e * kThreads + tid));
       }
-  __syncthreads();
-  const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
-  for (int e = threadIdx.x; e < R * 64; e += kThreads) {
-    // grad_a is written along the columns, grad_b along rho
-    const int rho = is_a ? e / 64 : e % R, c = is_a ? e % 64 : e / R;
-    if (rho >= r || n0 + c >= W) continue;
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < WT; ++k) s += part[(k * R + rho) * 64 + c];
-    if (is_a)
-      a.grad_a[((int64_t)ad * r + rho) * W + n0 + c] = s;
-    else
-      a.grad_b[((int64_t)ad * W + n0 + c) * r + rho] = scale * s;
+      write(open);
+    }
+    cluster_arrive();
   }
+  // adapters without tokens, shared by the cluster
+  clear();
+  for (int ad = rank; ad < a.plan.n; ad += C)
+    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
+  if (C > 1) cluster_wait();                                   // the others are done with this CTA's memory
 }
 
 template <typename KernelT>
@@ -452,12 +784,11 @@ cudaError_t set_smem(KernelT kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <int R, int M, bool BWD>
-cudaError_t run_rows(const LoraRows<bf16_t>& a, int64_t tiles, int cluster, cudaStream_t s) {
-  constexpr size_t smem = rows_smem<R, M>();
-  const cudaError_t e = set_smem(k_lora_rows<R, M, BWD>, smem);
+template <typename KernelT>
+cudaError_t run_rows(KernelT kernel, size_t smem, const LoraRows<bf16_t>& a, int64_t tiles, int cluster, cudaStream_t s) {
+  const cudaError_t e = set_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_cluster_pdl(k_lora_rows<R, M, BWD>, dim3((unsigned)(tiles * cluster)), dim3(kThreads), cluster, smem, s, a);
+  return launch_cluster_pdl(kernel, dim3((unsigned)(tiles * cluster)), dim3(kThreads), cluster, smem, s, a);
 }
 
 template <int R, bool BWD>
@@ -466,18 +797,21 @@ cudaError_t rows_m(LoraRows<bf16_t> a, const int* plan, int64_t T, int n, cudaSt
   a.plan = plan_view(plan, T, n, list);
   const int64_t tiles = plan_layout(T, n).cap[list];
   const int cluster = lora_cluster(tiles, a.K, a.N);
-  if (list == 1) return run_rows<R, 16, BWD>(a, tiles, cluster, s);
-  return run_rows<R, 64, BWD>(a, tiles, cluster, s);
+  if (list == 1) return run_rows(k_lora_rows16<R, BWD>, rows16_smem<R>(), a, tiles, cluster, s);
+  return run_rows(k_lora_rows64<R, BWD>, Rows64<R>::smem, a, tiles, cluster, s);
 }
 
 template <int R>
 cudaError_t run_wgrad(const LoraWgrad<bf16_t>& a, cudaStream_t s) {
-  constexpr int MT = R == 16 ? 1 : 2;
-  constexpr size_t smem = sizeof(float) * 64 * R * (kWarps / (R / (16 * MT)));
-  const cudaError_t e = set_smem(k_lora_wgrad<R>, smem);
+  using S = Wgrad<R>;
+  const cudaError_t e = set_smem(k_lora_wgrad<R>, S::smem);
   if (e != cudaSuccess) return e;
-  const int ba = a.grad_a ? (a.K + 63) / 64 : 0, bb = a.grad_b ? (a.N + 63) / 64 : 0;
-  return launch_pdl(k_lora_wgrad<R>, dim3((unsigned)(ba + bb), (unsigned)a.plan.n), dim3(kThreads), smem, s, a, ba);
+  const int ka = (a.K + S::kCols - 1) / S::kCols, nb = (a.N + S::kCols - 1) / S::kCols;
+  const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
+  // by both widths, so that a gradient does not depend on whether the other is asked for
+  const int cluster = lora_token_split(a.plan.T, ka + nb, S::kTok);
+  return launch_cluster_pdl(k_lora_wgrad<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, S::smem, s,
+                            a, ba);
 }
 
 template <bool BWD>

@@ -240,82 +240,145 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 }
 
 // ------------------------------------------------------------------- weight gradients
-// One CTA: 64 columns of x (grad_a) or of g (grad_b) over all tokens of one adapter, in token
-// order: 4 columns x R / 16 values of r per thread.
+// One cluster: 64 columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
+// plan's 64-token tiles evenly (TileShare); 4 columns x R / 16 values of r per thread. An
+// adapter whose tiles lie in several CTAs is written by the first of them, as in lora_bf16.cu.
+constexpr int kTok = 64;
+template <int R>
+constexpr size_t wgrad_smem() { return sizeof(float) * (kTok * (64 + 4) + kTok * (R + 4) + R * 64); }
+
 template <int R>
 __global__ void __launch_bounds__(kThreads) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
   constexpr int RT = R / 16, XS = 64 + 4, WS = R + 4;
-  __shared__ __align__(16) float xs[kKC * XS], ws[kKC * WS];
+  extern __shared__ __align__(16) float sm[];
+  float* const xs = sm;                                     // [kTok][XS]
+  float* const ws = sm + kTok * XS;                         // [kTok][WS]
+  float* const head = ws + kTok * WS;                       // [4 RT][kThreads]
+  __shared__ int2 desc[kWindow + 2];
   griddep_wait();
   if (!plan_matches(a.plan)) return;
-  const int ad = blockIdx.y, r = a.r, tid = threadIdx.x;
-  const bool is_a = (int)blockIdx.x < blocks_a;
-  const int n0 = 64 * (is_a ? blockIdx.x : blockIdx.x - blocks_a);
+  const unsigned C = cluster_size(), rank = cluster_rank();
+  const int r = a.r, tid = threadIdx.x, block = blockIdx.x / C;
+  const bool is_a = block < blocks_a;
+  const int n0 = 64 * (is_a ? block : block - blocks_a);
   const int W = is_a ? a.K : a.N;
   const float* const rows = is_a ? a.x : a.g;
   const float* const mid = is_a ? a.v : a.u;
-  const int beg = __ldg(a.plan.offsets + ad), end = __ldg(a.plan.offsets + ad + 1);
   // consecutive threads write consecutive elements: columns for grad_a, r for grad_b
   const int cg = is_a ? tid % 16 : tid / 16, rg = is_a ? tid / 16 : tid % 16;
+  const TileShare share(a.plan, rank, C);
   float acc[4][RT];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
-  constexpr int XL = kKC * 16 / kThreads, WL = (kKC * R / 4 + kThreads - 1) / kThreads;
+      for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
+  };
+  auto write = [&](int ad) {
+    const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rho = RT * rg + j, c = n0 + 4 * cg + i;
+        if (rho >= r || c >= W) continue;
+        if (is_a)
+          a.grad_a[((int64_t)ad * r + rho) * W + c] = acc[i][j];
+        else
+          a.grad_b[((int64_t)ad * W + c) * r + rho] = scale * acc[i][j];
+      }
+  };
+  constexpr int XL = kTok * 16 / kThreads, WL = kTok * R / 4 / kThreads;
   const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float4 xv[XL], wv[WL];
-  auto fetch = [&](int p0) {
+  auto fetch = [&](int p0, int tokens) {
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
-      const int e = tid + kThreads * i, pos = p0 + e / 16, c = n0 + e % 16 * 4;
-      xv[i] = (pos < end && c < W) ? ldg4(rows + (int64_t)__ldg(a.plan.order + pos) * W + c) : zero;
+      const int e = tid + kThreads * i, k = e / 16, c = n0 + e % 16 * 4;
+      xv[i] = (k < tokens && c < W) ? ldg4(rows + (int64_t)__ldg(a.plan.order + p0 + k) * W + c) : zero;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
-      const int e = tid + kThreads * i, k = e / (R / 4), pos = p0 + k, rho = e % (R / 4) * 4;
-      wv[i] = (k < kKC && pos < end && rho < r) ? ldg4(mid + (int64_t)__ldg(a.plan.order + pos) * r + rho) : zero;
+      const int e = tid + kThreads * i, k = e / (R / 4), rho = e % (R / 4) * 4;
+      wv[i] = (k < tokens && rho < r) ? ldg4(mid + (int64_t)__ldg(a.plan.order + p0 + k) * r + rho) : zero;
     }
   };
-  if (beg < end) fetch(beg);
-  for (int p0 = beg; p0 < end; p0 += kKC) {
+  clear();
+  int open = -1;                                            // adapter whose sums go on in the next CTA
+  bool from_before = false;                                 // the sum at hand began in an earlier CTA
+  for (int w0 = share.lo; w0 < share.hi; w0 += kWindow) {
+    const int count = min(kWindow, share.hi - w0);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      const int e = tid + kThreads * i;
-      *reinterpret_cast<float4*>(xs + e / 16 * XS + e % 16 * 4) = xv[i];
-    }
-#pragma unroll
-    for (int i = 0; i < WL; ++i) {
-      const int e = tid + kThreads * i, k = e / (R / 4);
-      if (k < kKC) *reinterpret_cast<float4*>(ws + k * WS + e % (R / 4) * 4) = wv[i];
-    }
+    share.window(a.plan, w0, desc);
     __syncthreads();
-    if (p0 + kKC < end) fetch(p0 + kKC);
+    if (w0 == share.lo) from_before = desc[0].y == desc[1].y;
+    fetch(desc[1].x, desc[2].x - desc[1].x);
+    for (int i = 0; i < count; ++i) {
+      __syncthreads();                                      // the last tile is consumed
+#pragma unroll
+      for (int h = 0; h < XL; ++h) {
+        const int e = tid + kThreads * h;
+        *reinterpret_cast<float4*>(xs + e / 16 * XS + e % 16 * 4) = xv[h];
+      }
+#pragma unroll
+      for (int h = 0; h < WL; ++h) {
+        const int e = tid + kThreads * h;
+        *reinterpret_cast<float4*>(ws + e / (R / 4) * WS + e % (R / 4) * 4) = wv[h];
+      }
+      __syncthreads();
+      const int tokens = desc[i + 2].x - desc[i + 1].x, ad = desc[i + 1].y;
+      if (i + 1 < count) fetch(desc[i + 2].x, desc[i + 3].x - desc[i + 2].x);
 #pragma unroll 8
-    for (int k = 0; k < kKC; ++k) {
-      float xr[4], wr[RT];
-      lds<4>(xs + k * XS + 4 * cg, xr);
-      lds<RT>(ws + k * WS + RT * rg, wr);
+      for (int k = 0; k < tokens; ++k) {
+        float xr[4], wr[RT];
+        lds<4>(xs + k * XS + 4 * cg, xr);
+        lds<RT>(ws + k * WS + RT * rg, wr);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(xr[i], wr[j], acc[i][j]);
+          for (int j = 0; j < RT; ++j) acc[x][j] = fmaf(xr[x], wr[j], acc[x][j]);
+      }
+      const bool goes_on = desc[i + 2].y == ad;             // the next tile is the same adapter's
+      if (w0 + i + 1 == share.hi && goes_on && !from_before) {
+        open = ad;                                          // its sums stay here
+      } else if (!goes_on || w0 + i + 1 == share.hi) {
+        if (from_before) {                                  // an earlier CTA writes it
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) head[(x * RT + j) * kThreads + tid] = acc[x][j];
+          from_before = false;
+        } else {
+          write(ad);
+        }
+        clear();
+      }
     }
   }
   griddep_launch_dependents();
-  const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (open >= 0) {
+      // the CTAs after this one up to the adapter's end hold its other sums
+      for (unsigned k = rank + 1; k < C; ++k) {
+        const int klo = (int)((int64_t)share.all * k / C), khi = (int)((int64_t)share.all * (k + 1) / C);
+        if (klo == khi) continue;                           // no tiles there
+        if (__ldg(a.plan.tiles + klo).y != open) break;
+        const uint32_t src = map_rank(head, k);
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rho = RT * rg + j, c = n0 + 4 * cg + i;
-      if (rho >= r || c >= W) continue;
-      if (is_a)
-        a.grad_a[((int64_t)ad * r + rho) * W + c] = acc[i][j];
-      else
-        a.grad_b[((int64_t)ad * W + c) * r + rho] = scale * acc[i][j];
+          for (int j = 0; j < RT; ++j) acc[i][j] += ld_cluster_f1(src + 4 * ((i * RT + j) * kThreads + tid));
+      }
+      write(open);
     }
+    cluster_arrive();
+  }
+  clear();
+  for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens
+    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
+  if (C > 1) cluster_wait();                                // the others are done with this CTA's memory
 }
 
 template <int R, int M, bool BWD>
@@ -350,8 +413,18 @@ cudaError_t rows_r(const LoraRows<float>& a, const int* plan, int64_t T, int n, 
 
 template <int R>
 cudaError_t run_wgrad(const LoraWgrad<float>& a, cudaStream_t s) {
-  const int ba = a.grad_a ? (a.K + 63) / 64 : 0, bb = a.grad_b ? (a.N + 63) / 64 : 0;
-  return launch_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)(ba + bb), (unsigned)a.plan.n), dim3(kThreads), 0, s, a, ba);
+  const int ka = (a.K + 63) / 64, nb = (a.N + 63) / 64;
+  const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
+  constexpr size_t smem = wgrad_smem<R>();
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_lora_wgrad_f32<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  // by both widths, so that a gradient does not depend on whether the other is asked for
+  const int cluster = lora_token_split(a.plan.T, ka + nb, kTok);
+  return launch_cluster_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, smem, s,
+                            a, ba);
 }
 
 }  // namespace

@@ -62,7 +62,7 @@ static LoraWgrad<T> wgrad_args(const void* g, const void* x, const float* u, con
   a.u = u, a.v = v, a.scale = scale;
   a.grad_a = grad_a, a.grad_b = grad_b;
   a.K = K, a.N = N, a.r = r;
-  a.plan = plan_view(plan, tokens, n, 0);
+  a.plan = plan_view(plan, tokens, n, 2);
   return a;
 }
 

@@ -22,6 +22,16 @@ inline int lora_cluster(int64_t tiles, int K, int N) {
   return c;
 }
 
+// CTAs per cluster of the low-rank weight gradients, which share the batch's tokens: as many as
+// keep the grid of `blocks` clusters within about three CTAs per SM (one wave), at most 8, and
+// no more than the batch has pieces of `chunk` tokens.
+inline int lora_token_split(int64_t T, int blocks, int chunk) {
+  int64_t c = 444 / blocks;
+  const int64_t pieces = (T + chunk - 1) / chunk;
+  if (c > pieces) c = pieces;
+  return c < 1 ? 1 : (c > 8 ? 8 : (int)c);
+}
+
 // Tokens per CTA of the many-adapter layer kernels at p <= 512: as layer_x_tokens for T
 // tokens, but 1 while the mean group is below 2 and at most 2 below 4 (a CTA's tokens share
 // one adapter, and unfilled places cost their transforms).
