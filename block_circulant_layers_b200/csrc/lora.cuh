@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "adapter_plan.h"
 #include "internal.h"
 #include "packed_fft.cuh"
@@ -108,6 +110,18 @@ struct TileShare {
   }
 };
 
+// Asynchronous copies to shared memory.
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes to shared memory; zeros when !in (src is then not read, but must be a valid pointer).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Cluster of this CTA (one-dimensional).
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned v;
@@ -136,6 +150,50 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
+}
+
+// Sum over the cluster's CTAs of the four floats at `p`, in rank order; the loads go out together.
+__device__ __forceinline__ float4 cluster_sum_f4(const float* p, unsigned C) {
+  float4 v[8];
+#pragma unroll
+  for (unsigned c = 0; c < 8; ++c)
+    if (c < C) v[c] = ld_cluster_f4(map_rank(p, c));
+  float4 s = v[0];
+#pragma unroll
+  for (unsigned c = 1; c < 8; ++c)
+    if (c < C) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
+  return s;
+}
+
+// Adds the N sums of this thread that CTA `rank` left at head[e][thread].
+template <int N>
+__device__ __forceinline__ void add_from(float (&acc)[N], const float* head, unsigned rank) {
+  const uint32_t src = map_rank(head, rank) + 4 * threadIdx.x;
+  constexpr int B = N < 16 ? N : 16;                          // loads in flight
+#pragma unroll
+  for (int e0 = 0; e0 < N; e0 += B) {
+    float v[B];
+#pragma unroll
+    for (int e = 0; e < B; ++e) v[e] = ld_cluster_f1(src + 4 * blockDim.x * (e0 + e));
+#pragma unroll
+    for (int e = 0; e < B; ++e) acc[e0 + e] += v[e];
+  }
+}
+
+// Allows KERNEL `bytes` of dynamic shared memory on the current device. The attribute stays with
+// the loaded kernel, so it is set once per device (bytes is the same in every call).
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (set.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // launch_pdl with the grid cut into clusters of `cluster` CTAs along x.

@@ -82,7 +82,7 @@ constexpr size_t rows16_smem() {
 
 // R: r rounded up to 16, 32, 64 or 128.
 template <int R, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_lora_rows16(LoraRows<bf16_t> a) {
+__global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) k_lora_rows16(LoraRows<bf16_t> a) {
   constexpr int M = 16, WK = kWarps;                           // the warps share the K columns
   constexpr int NJ = R / 8;
   constexpr int V = R / 8;                                     // r values per lane of a w1 row, backward
@@ -211,15 +211,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows16(LoraRows<bf16_t> a) {
     // of two bf16, hi + lo (16 mantissa bits), so its rounding stays far below the output's
     const float scale = a.scale ? __ldg(a.scale + ad) : 1.0f;
     for (int e = 4 * threadIdx.x; e < M * R; e += 4 * kThreads) {
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (C > 1) {
-        for (unsigned c = 0; c < C; ++c) {
-          const float4 v = ld_cluster_f4(map_rank(part + e, c));
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-      } else {
-        s = *reinterpret_cast<const float4*>(part + e);
-      }
+      const float4 s = C > 1 ? cluster_sum_f4(part + e, C) : *reinterpret_cast<const float4*>(part + e);
       const int t = e / R, c = e % R;
       // columns beyond r stay zero even where a row holds an infinity (0 x inf)
       const float4 ss = c < r ? make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w)
@@ -313,17 +305,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows16(LoraRows<bf16_t> a) {
   if (adapted && C > 1) cluster_wait();                        // the others are done with this CTA's memory
 }
 
-// ------------------------------------------------------------- staging and fragments
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes to shared memory; zeros when !in (src is then not read, but must be a valid pointer).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// ----------------------------------------------------------------- tiles and fragments
 __device__ __forceinline__ void ldsm4(uint32_t (&v)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
@@ -496,15 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
     // of two bf16, hi + lo (16 mantissa bits), so its rounding stays far below the output's
     const float scale = a.scale ? __ldg(a.scale + ad) : 1.0f;
     for (int e = 4 * tid; e < M * R; e += 4 * kThreads) {
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (C > 1) {
-        for (unsigned c = 0; c < C; ++c) {
-          const float4 v = ld_cluster_f4(map_rank(part + e, c));
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-      } else {
-        s = *reinterpret_cast<const float4*>(part + e);
-      }
+      const float4 s = C > 1 ? cluster_sum_f4(part + e, C) : *reinterpret_cast<const float4*>(part + e);
       const int t = e / R, c = e % R;
       // columns beyond r stay zero even where a row holds an infinity (0 x inf)
       const float4 ss = c < r ? make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w)
@@ -582,13 +556,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 // columns and every rho (half of them at r > 64), so no sums are shared inside a CTA. An adapter whose tiles lie in
 // several CTAs is written by the first of them, which adds the others' sums in rank order
 // through distributed shared memory.
-// Tiles pass through a ring of cp.async stages: a tile's token numbers are requested four
-// steps ahead, its rows two steps ahead.
+// Tiles pass through a ring of cp.async stages: a tile's rows are requested one or two steps
+// ahead, its token numbers two steps before that.
 // mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits
 // (24 mantissa bits), since the gradients are fp32.
 template <int R>
 struct Wgrad {
-  static constexpr int kCols = R <= 64 ? 128 : 64, kTok = 64, kStages = 3, kOrders = 8;
+  static constexpr int kCols = R <= 64 ? 128 : 64, kTok = 64, kOrders = 8;
+  static constexpr int kStages = R <= 32 ? 2 : 3, kAhead = kStages - 1;   // row tiles requested ahead
+  static constexpr int kPerSM = R == 16 ? 3 : (R == 32 ? 2 : 1);          // CTAs that fit
   static constexpr int kWC = kCols / 16, kNI = R / 16 / (kWarps / kWC);   // column groups; rho tiles per warp
   static constexpr int kRowBytes = kTok * kCols * 2;
   static constexpr int kStage = kRowBytes + kTok * R * 4;     // rows, and mid in fp32
@@ -598,7 +574,7 @@ struct Wgrad {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, R == 16 ? 3 : (R == 32 ? 2 : 1))
+__global__ void __launch_bounds__(kThreads, Wgrad<R>::kPerSM)
 k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   using S = Wgrad<R>;
   constexpr int COLS = S::kCols, UNITS = COLS / 8, NI = S::kNI;
@@ -691,18 +667,18 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
     cp_commit();
     cp_wait<0>();
     __syncthreads();
-    request(0);
-    request_order(2);
-    cp_commit();
-    request(1);
-    request_order(3);
-    cp_commit();
+#pragma unroll
+    for (int s = 0; s < S::kAhead; ++s) {
+      request(s);
+      request_order(s + 2);
+      cp_commit();
+    }
     if (w0 == share.lo) from_before = desc[0].y == desc[1].y;
     for (int i = 0; i < count; ++i) {
-      cp_wait<1>();                                            // all but the last request: rows i, order i + 2
+      cp_wait<S::kAhead - 1>();                                // rows i and order i + kAhead have arrived
       __syncthreads();
-      request(i + 2);
-      request_order(i + 4);
+      request(i + S::kAhead);
+      request_order(i + S::kAhead + 2);
       cp_commit();
       const unsigned char* const stage = ring + i % S::kStages * S::kStage;
 #pragma unroll
@@ -763,9 +739,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
         const int klo = (int)((int64_t)share.all * k / C), khi = (int)((int64_t)share.all * (k + 1) / C);
         if (klo == khi) continue;                              // no tiles there
         if (__ldg(a.plan.tiles + klo).y != open) break;
-        const uint32_t src = map_rank(head, k);
-#pragma unroll
-        for (int e = 0; e < NA; ++e) acc[e] += ld_cluster_f1(src + 4 * (e * kThreads + tid));
+        add_from(acc, head, k);
       }
       write(open);
     }
@@ -778,17 +752,11 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   if (C > 1) cluster_wait();                                   // the others are done with this CTA's memory
 }
 
-template <typename KernelT>
-cudaError_t set_smem(KernelT kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
-template <typename KernelT>
-cudaError_t run_rows(KernelT kernel, size_t smem, const LoraRows<bf16_t>& a, int64_t tiles, int cluster, cudaStream_t s) {
-  const cudaError_t e = set_smem(kernel, smem);
+template <auto KERNEL>
+cudaError_t run_rows(size_t smem, const LoraRows<bf16_t>& a, int64_t tiles, int cluster, cudaStream_t s) {
+  const cudaError_t e = allow_smem<KERNEL>(smem);
   if (e != cudaSuccess) return e;
-  return launch_cluster_pdl(kernel, dim3((unsigned)(tiles * cluster)), dim3(kThreads), cluster, smem, s, a);
+  return launch_cluster_pdl(KERNEL, dim3((unsigned)(tiles * cluster)), dim3(kThreads), cluster, smem, s, a);
 }
 
 template <int R, bool BWD>
@@ -796,20 +764,20 @@ cudaError_t rows_m(LoraRows<bf16_t> a, const int* plan, int64_t T, int n, cudaSt
   const int list = lora_list(T, n);
   a.plan = plan_view(plan, T, n, list);
   const int64_t tiles = plan_layout(T, n).cap[list];
-  const int cluster = lora_cluster(tiles, a.K, a.N);
-  if (list == 1) return run_rows(k_lora_rows16<R, BWD>, rows16_smem<R>(), a, tiles, cluster, s);
-  return run_rows(k_lora_rows64<R, BWD>, Rows64<R>::smem, a, tiles, cluster, s);
+  const int cluster = lora_cluster(tiles, list, false, a.K, a.N);
+  if (list == 1) return run_rows<k_lora_rows16<R, BWD>>(rows16_smem<R>(), a, tiles, cluster, s);
+  return run_rows<k_lora_rows64<R, BWD>>(Rows64<R>::smem, a, tiles, cluster, s);
 }
 
 template <int R>
 cudaError_t run_wgrad(const LoraWgrad<bf16_t>& a, cudaStream_t s) {
   using S = Wgrad<R>;
-  const cudaError_t e = set_smem(k_lora_wgrad<R>, S::smem);
+  const cudaError_t e = allow_smem<k_lora_wgrad<R>>(S::smem);
   if (e != cudaSuccess) return e;
   const int ka = (a.K + S::kCols - 1) / S::kCols, nb = (a.N + S::kCols - 1) / S::kCols;
   const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
   // by both widths, so that a gradient does not depend on whether the other is asked for
-  const int cluster = lora_token_split(a.plan.T, ka + nb, S::kTok);
+  const int cluster = lora_token_split(a.plan.T, ka + nb, S::kTok, S::kPerSM);
   return launch_cluster_pdl(k_lora_wgrad<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, S::smem, s,
                             a, ba);
 }

@@ -1,8 +1,9 @@
 // Low-rank adapters of many requests, fp32: rows kernel (forward, grad_x) and weight
 // gradients. The same split as lora_bf16.cu (one cluster per tile of the plan, one launch),
 // with the products as fp32 FMAs on register tiles fed from shared memory: the parity bar of
-// fp32 leaves no room for tf32 operands. Operand chunks lie in shared memory with the
-// contraction index outermost, so a thread's rows and columns are one vector each.
+// fp32 leaves no room for tf32 operands. Steps of 32 contraction indices, then of 64 output
+// columns, pass through one ring of cp.async stages; operands keep their own row order, padded
+// by 16 bytes a row, and are read 4 contraction indices at a time.
 #include "lora.cuh"
 
 #include "many_policy.h"
@@ -12,7 +13,8 @@ namespace rdfft {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKC = 32;                        // contraction indices per chunk
+constexpr int kKC = 32;                        // contraction indices per step
+constexpr int kNC = 64;                        // output columns per step
 
 // N consecutive floats of shared memory.
 template <int N>
@@ -32,29 +34,28 @@ __device__ __forceinline__ void lds(const float* p, float (&v)[N]) {
 }
 
 __device__ __forceinline__ float4 ldg4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ void put(float* p, int stride, float4 v) {
-  p[0] = v.x, p[stride] = v.y, p[2 * stride] = v.z, p[3 * stride] = v.w;
-}
 
-template <int R, int M>
+template <int R, int M, bool BWD>
 struct RowsShape {
-  static constexpr int KG = 64 / M;                         // thread groups that share a chunk's indices
-  static constexpr int XS = M + 4, WS = R + 4;              // padded strides
-  static constexpr int NC = 4096 / M, NS = NC + 4;          // output columns per pass
-  static constexpr int kChunk = kKC * (XS + WS), kExpand = kKC * NS, kPart = KG * M * R;
-  static constexpr int kStage = kChunk > kExpand ? kChunk : kExpand;
-  static constexpr size_t smem = sizeof(float) * (size_t)(kStage + kPart + R * XS);
+  static constexpr int KG = 64 / M;                         // thread groups that share a step's indices
+  static constexpr int XS = kKC + 4;                        // padded strides: in,
+  static constexpr int W1S = BWD ? R + 4 : kKC + 4;         // w1 (backward: contraction index outermost),
+  static constexpr int W2S = BWD ? kNC + 4 : R + 4;         // w2 (the same),
+  static constexpr int MS = R + 4;                          // mid
+  static constexpr int kFirst = M * XS + (BWD ? kKC : R) * W1S, kSecond = (BWD ? R : kNC) * W2S;
+  static constexpr int kStage = kFirst > kSecond ? kFirst : kSecond;
+  static constexpr int kStages = R <= 64 ? 4 : 3;
+  static constexpr int kPart = KG * M * R;
+  static constexpr size_t smem = sizeof(float) * (size_t)(kStage * kStages + kPart + M * MS);
 };
 
 template <int R, int M, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
-  using S = RowsShape<R, M>;
+  using S = RowsShape<R, M, BWD>;
   constexpr int RT = R / 16;                                // r values per thread
-  extern __shared__ __align__(16) float sm[];
-  float* const xs = sm;                                     // [kKC][XS]
-  float* const ws = sm + kKC * S::XS;                       // [kKC][WS]
-  float* const part = sm + S::kStage;                       // [KG][M][R]
-  float* const mid = part + S::kPart;                       // [R][XS]
+  extern __shared__ __align__(16) float sm[];               // ring
+  float* const part = sm + S::kStage * S::kStages;          // [KG][M][R]
+  float* const mid = part + S::kPart;                       // [M][MS]
 
   griddep_wait();
   if (!plan_matches(a.plan)) return;
@@ -67,80 +68,115 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   const int tid = threadIdx.x, K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
 
+  // this CTA's steps: [0, n1) of 32 columns of in and w1, then [n1, n1 + n2) of 64 of w2
+  const int ks = (K + kKC - 1) / kKC, ns = (N + kNC - 1) / kNC;
+  const int k_first = (int)((int64_t)ks * rank / C), n_first = (int)((int64_t)ns * rank / C);
+  const int n1 = adapted ? (int)((int64_t)ks * (rank + 1) / C) - k_first : 0;
+  const int n2 = (a.out != nullptr && (adapted || a.base != a.out)) ? (int)((int64_t)ns * (rank + 1) / C) - n_first : 0;
+  const float* const w1 = a.w1 + (adapted ? (int64_t)ad * r * K : 0);
+  const float* const w2 = a.w2 + (adapted ? (int64_t)ad * r * N : 0);
+  constexpr int XL = (M * 8 + kThreads - 1) / kThreads;
+  int xtok[XL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) {
+    const int t = (tid + kThreads * i) / 8;
+    xtok[i] = t < m ? __ldg(a.plan.order + pos0 + t) : -1;
+  }
+  auto request = [&](int step) {
+    if (adapted && step < n1 + n2) {
+      const uint32_t dst = smem_addr(sm + step % S::kStages * S::kStage);
+      if (step < n1) {
+        const int k0 = kKC * (k_first + step);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+          const int e = tid + kThreads * i, k = k0 + e % 8 * 4;
+          const bool in = xtok[i] >= 0 && k < K;
+          if (e < M * 8) cp16(dst + (e / 8 * S::XS + e % 8 * 4) * 4, in ? a.in + (int64_t)xtok[i] * K + k : a.in, in);
+        }
+        const uint32_t wdst = dst + M * S::XS * 4;
+#pragma unroll
+        for (int i = 0; i < (R * 8 + kThreads - 1) / kThreads; ++i) {
+          const int e = tid + kThreads * i;
+          if (R * 8 < kThreads && e >= R * 8) break;
+          if constexpr (!BWD) {
+            const int rho = e / 8, k = k0 + e % 8 * 4;
+            const bool in = rho < r && k < K;
+            cp16(wdst + (rho * S::W1S + e % 8 * 4) * 4, in ? w1 + (int64_t)rho * K + k : w1, in);
+          } else {
+            const int k = k0 + e / (R / 4), rho = e % (R / 4) * 4;
+            const bool in = rho < r && k < K;
+            cp16(wdst + (e / (R / 4) * S::W1S + rho) * 4, in ? w1 + (int64_t)k * r + rho : w1, in);
+          }
+        }
+      } else {
+        const int n0 = kNC * (n_first + step - n1);
+#pragma unroll
+        for (int i = 0; i < kNC * R / 4 / kThreads; ++i) {
+          const int e = tid + kThreads * i;
+          if constexpr (!BWD) {
+            const int c = e / (R / 4), rho = e % (R / 4) * 4;
+            const bool in = n0 + c < N && rho < r;
+            cp16(dst + (c * S::W2S + rho) * 4, in ? w2 + (int64_t)(n0 + c) * r + rho : w2, in);
+          } else {
+            const int rho = e / (kNC / 4), c = e % (kNC / 4) * 4;
+            const bool in = n0 + c < N && rho < r;
+            cp16(dst + (rho * S::W2S + c) * 4, in ? w2 + (int64_t)rho * N + n0 + c : w2, in);
+          }
+        }
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) request(s);
+
   if (adapted) {
-    // ---- mid = in w1^T over this CTA's units of 32 columns: 4 rows x RT values per thread
+    // ---- mid = in w1^T: 4 rows x RT values per thread, rows 4 rg + i, values cg + 16 j (backward RT cg + j)
     constexpr int GT = 4 * M;                               // threads of one k group
     const int kg = tid / GT, rg = tid % GT / 16, cg = tid % 16;
-    const int units = (K + 31) / 32;
-    const int u0 = (int)((int64_t)units * rank / C), u1 = (int)((int64_t)units * (rank + 1) / C);
-    const float* const w1 = a.w1 + (int64_t)ad * r * K;
     float acc[4][RT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
-    constexpr int XL = (M * 8 + kThreads - 1) / kThreads, WL = (R * 8 + kThreads - 1) / kThreads;
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    int64_t xrow[XL];
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      const int t = (tid + kThreads * i) / 8;
-      xrow[i] = t < m ? (int64_t)__ldg(a.plan.order + pos0 + t) * K : -1;
-    }
-    float4 xv[XL], wv[WL];
-    auto fetch = [&](int u) {
-      const int k0 = 32 * u;
-#pragma unroll
-      for (int i = 0; i < XL; ++i) {
-        const int k = k0 + (tid + kThreads * i) % 8 * 4;
-        xv[i] = (xrow[i] >= 0 && k < K) ? ldg4(a.in + xrow[i] + k) : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < WL; ++i) {
-        const int e = tid + kThreads * i;
-        if constexpr (!BWD) {
-          const int rho = e / 8, k = k0 + e % 8 * 4;
-          wv[i] = (rho < r && k < K) ? ldg4(w1 + (int64_t)rho * K + k) : zero;
-        } else {
-          const int k = k0 + e / (R / 4), rho = e % (R / 4) * 4;
-          wv[i] = (e < R * 8 && rho < r && k < K) ? ldg4(w1 + (int64_t)k * r + rho) : zero;
-        }
-      }
-    };
-    if (u0 < u1) fetch(u0);
-    for (int u = u0; u < u1; ++u) {
-      __syncthreads();                                      // the previous chunk is consumed
-#pragma unroll
-      for (int i = 0; i < XL; ++i) {
-        const int e = tid + kThreads * i;
-        if (e < M * 8) put(xs + e % 8 * 4 * S::XS + e / 8, S::XS, xv[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < WL; ++i) {
-        const int e = tid + kThreads * i;
-        if (e >= R * 8) continue;
-        if constexpr (!BWD)
-          put(ws + e % 8 * 4 * S::WS + e / 8, S::WS, wv[i]);
-        else
-          *reinterpret_cast<float4*>(ws + e / (R / 4) * S::WS + e % (R / 4) * 4) = wv[i];
-      }
+    for (int step = 0; step < n1; ++step) {
+      cp_wait<S::kStages - 2>();
       __syncthreads();
-      if (u + 1 < u1) fetch(u + 1);
-#pragma unroll 8
-      for (int k = kg * (kKC / S::KG); k < (kg + 1) * (kKC / S::KG); ++k) {
-        float xr[4], wr[RT];
-        lds<4>(xs + k * S::XS + 4 * rg, xr);
-        lds<RT>(ws + k * S::WS + RT * cg, wr);
+      request(step + S::kStages - 1);
+      const float* const xs = sm + step % S::kStages * S::kStage;
+      const float* const ws = xs + M * S::XS;
+#pragma unroll 2
+      for (int k = kg * (kKC / S::KG); k < (kg + 1) * (kKC / S::KG); k += 4) {
+        float xr[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) lds<4>(xs + (4 * rg + i) * S::XS + k, xr[i]);
+        if constexpr (!BWD) {
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(xr[i], wr[j], acc[i][j]);
+          for (int j = 0; j < RT; ++j) {
+            float wr[4];
+            lds<4>(ws + (cg + 16 * j) * S::W1S + k, wr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j] = fmaf(xr[i][e], wr[e], acc[i][j]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float wr[RT];
+            lds<RT>(ws + (k + e) * S::W1S + RT * cg, wr);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(xr[i][e], wr[j], acc[i][j]);
+          }
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) part[(kg * M + 4 * rg + i) * R + RT * cg + j] = acc[i][j];
+      for (int j = 0; j < RT; ++j) part[(kg * M + 4 * rg + i) * R + (BWD ? RT * cg + j : cg + 16 * j)] = acc[i][j];
     __syncthreads();
     if constexpr (S::KG > 1) {
       for (int e = tid; e < M * R; e += kThreads) {
@@ -159,24 +195,16 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
     // the cluster's sum in rank order, every CTA for itself
     const float scale = a.scale ? __ldg(a.scale + ad) : 1.0f;
     for (int e = 4 * tid; e < M * R; e += 4 * kThreads) {
-      float4 s = zero;
-      if (C > 1) {
-        for (unsigned c = 0; c < C; ++c) {
-          const float4 v = ld_cluster_f4(map_rank(part + e, c));
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-      } else {
-        s = *reinterpret_cast<const float4*>(part + e);
-      }
+      const float4 s = C > 1 ? cluster_sum_f4(part + e, C) : *reinterpret_cast<const float4*>(part + e);
       const int t = e / R, c = e % R;
       // columns beyond r stay zero even where a row holds an infinity (0 x inf)
-      const float4 ss = c < r ? make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w) : zero;
+      const float4 ss = c < r ? make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (a.mid && t < m && c < r && (unsigned)(t % C) == rank)
         *reinterpret_cast<float4*>(a.mid + (int64_t)__ldg(a.plan.order + pos0 + t) * r + c) = BWD ? ss : s;
-      put(mid + c * S::XS + t, S::XS, ss);
+      *reinterpret_cast<float4*>(mid + t * S::MS + c) = ss;
     }
     if (C > 1) cluster_arrive();                            // done with the others' memory
-    __syncthreads();
   } else if (a.mid) {
     for (int e = tid; e < m * r; e += kThreads) {           // tokens without an adapter: mid is zero
       const int t = e / r;
@@ -185,57 +213,70 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   }
   griddep_launch_dependents();
 
-  // ---- out = base + mid w2^T over this CTA's columns: 4 rows x 4 columns per thread
-  if (a.out != nullptr && (adapted || a.base != a.out)) {
-    const int rg = tid % (M / 4), cg = tid / (M / 4);
-    const int groups = (N + S::NC - 1) / S::NC;
-    const int g0 = (int)((int64_t)groups * rank / C), g1 = (int)((int64_t)groups * (rank + 1) / C);
-    const float* const w2 = a.w2 + (int64_t)(adapted ? ad : 0) * r * N;
-    for (int gr = g0; gr < g1; ++gr) {
-      const int n0 = S::NC * gr, c = n0 + 4 * cg;
-      float acc[4][4];
-      int64_t orow[4];
+  // ---- out = base + mid w2^T: RM rows x 4 columns per thread, columns cg + 16 j (backward 4 cg + j)
+  constexpr int RM = M / 16;
+  const int rg = tid / 16, cg = tid % 16;
+  int otok[RM];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * rg + i;
-        orow[i] = (t < m && c < N) ? (int64_t)__ldg(a.plan.order + pos0 + t) * N + c : -1;
-        float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (a.base && orow[i] >= 0) b = *reinterpret_cast<const float4*>(a.base + orow[i]);
-        acc[i][0] = b.x, acc[i][1] = b.y, acc[i][2] = b.z, acc[i][3] = b.w;
+  for (int i = 0; i < RM; ++i) otok[i] = RM * rg + i < m ? __ldg(a.plan.order + pos0 + RM * rg + i) : -1;
+  for (int step = n1; step < n1 + n2; ++step) {
+    const int n0 = kNC * (n_first + step - n1);
+    float acc[RM][4];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = n0 + (BWD ? 4 * cg + j : cg + 16 * j);
+        acc[i][j] = (a.base && otok[i] >= 0 && c < N) ? a.base[(int64_t)otok[i] * N + c] : 0.0f;
       }
-      for (int r0 = 0; adapted && r0 < r; r0 += kKC) {
-        __syncthreads();
-        for (int e = tid; e < S::NC * 8; e += kThreads) {
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if constexpr (!BWD) {
-            const int cc = e / 8, rho = r0 + e % 8 * 4;
-            if (n0 + cc < N && rho < r) v = ldg4(w2 + (int64_t)(n0 + cc) * r + rho);
-            put(sm + e % 8 * 4 * S::NS + cc, S::NS, v);
-          } else {
-            const int rho = e / (S::NC / 4), cc = e % (S::NC / 4) * 4;
-            if (n0 + cc < N && r0 + rho < r) v = ldg4(w2 + (int64_t)(r0 + rho) * N + n0 + cc);
-            *reinterpret_cast<float4*>(sm + rho * S::NS + cc) = v;
+    cp_wait<S::kStages - 2>();
+    __syncthreads();                                        // the stage, and at first mid, is complete
+    request(step + S::kStages - 1);
+    const float* const ws = sm + step % S::kStages * S::kStage;
+    if (adapted) {
+#pragma unroll 2
+      for (int k = 0; k < R; k += 4) {
+        float mr[RM][4];
+#pragma unroll
+        for (int i = 0; i < RM; ++i) lds<4>(mid + (RM * rg + i) * S::MS + k, mr[i]);
+        if constexpr (!BWD) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float wr[4];
+            lds<4>(ws + (cg + 16 * j) * S::W2S + k, wr);
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j] = fmaf(mr[i][e], wr[e], acc[i][j]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float wr[4];
+            lds<4>(ws + (k + e) * S::W2S + 4 * cg, wr);
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mr[i][e], wr[j], acc[i][j]);
           }
         }
-        __syncthreads();
-        const int kn = min(kKC, R - r0);
-#pragma unroll 8
-        for (int k = 0; k < kn; ++k) {
-          float mr[4], wr[4];
-          lds<4>(mid + (r0 + k) * S::XS + 4 * rg, mr);
-          lds<4>(sm + k * S::NS + 4 * cg, wr);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mr[i], wr[j], acc[i][j]);
-        }
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (orow[i] >= 0)
-          *reinterpret_cast<float4*>(a.out + orow[i]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    for (int i = 0; i < RM; ++i) {
+      if (otok[i] < 0) continue;
+      float* const o = a.out + (int64_t)otok[i] * N + n0;
+      if constexpr (BWD) {
+        if (n0 + 4 * cg < N)
+          *reinterpret_cast<float4*>(o + 4 * cg) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + cg + 16 * j < N) o[cg + 16 * j] = acc[i][j];
+      }
     }
   }
+  cp_wait<0>();
   if (adapted && C > 1) cluster_wait();                     // the others are done with this CTA's memory
 }
 
@@ -245,10 +286,12 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 // adapter whose tiles lie in several CTAs is written by the first of them, as in lora_bf16.cu.
 constexpr int kTok = 64;
 template <int R>
+constexpr int wgrad_per_sm() { return R <= 32 ? 3 : (R == 64 ? 2 : 1); }
+template <int R>
 constexpr size_t wgrad_smem() { return sizeof(float) * (kTok * (64 + 4) + kTok * (R + 4) + R * 64); }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
+__global__ void __launch_bounds__(kThreads, wgrad_per_sm<R>()) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
   constexpr int RT = R / 16, XS = 64 + 4, WS = R + 4;
   extern __shared__ __align__(16) float sm[];
   float* const xs = sm;                                     // [kTok][XS]
@@ -365,11 +408,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_wgrad_f32(LoraWgrad<float> a,
         const int klo = (int)((int64_t)share.all * k / C), khi = (int)((int64_t)share.all * (k + 1) / C);
         if (klo == khi) continue;                           // no tiles there
         if (__ldg(a.plan.tiles + klo).y != open) break;
-        const uint32_t src = map_rank(head, k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] += ld_cluster_f1(src + 4 * ((i * RT + j) * kThreads + tid));
+        add_from(*reinterpret_cast<float(*)[4 * RT]>(acc), head, k);
       }
       write(open);
     }
@@ -383,12 +422,9 @@ __global__ void __launch_bounds__(kThreads) k_lora_wgrad_f32(LoraWgrad<float> a,
 
 template <int R, int M, bool BWD>
 cudaError_t run_rows(const LoraRows<float>& a, int64_t tiles, int cluster, cudaStream_t s) {
-  constexpr size_t smem = RowsShape<R, M>::smem;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_lora_rows_f32<R, M, BWD>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  constexpr size_t smem = RowsShape<R, M, BWD>::smem;
+  const cudaError_t e = allow_smem<k_lora_rows_f32<R, M, BWD>>(smem);
+  if (e != cudaSuccess) return e;
   return launch_cluster_pdl(k_lora_rows_f32<R, M, BWD>, dim3((unsigned)(tiles * cluster)), dim3(kThreads), cluster,
                             smem, s, a);
 }
@@ -398,7 +434,7 @@ cudaError_t rows_m(LoraRows<float> a, const int* plan, int64_t T, int n, cudaStr
   const int list = lora_list(T, n);
   a.plan = plan_view(plan, T, n, list);
   const int64_t tiles = plan_layout(T, n).cap[list];
-  const int cluster = lora_cluster(tiles, a.K, a.N);
+  const int cluster = lora_cluster(tiles, list, true, a.K, a.N);
   if (list == 1) return run_rows<R, 16, BWD>(a, tiles, cluster, s);
   return run_rows<R, 64, BWD>(a, tiles, cluster, s);
 }
@@ -416,13 +452,10 @@ cudaError_t run_wgrad(const LoraWgrad<float>& a, cudaStream_t s) {
   const int ka = (a.K + 63) / 64, nb = (a.N + 63) / 64;
   const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
   constexpr size_t smem = wgrad_smem<R>();
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_lora_wgrad_f32<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<k_lora_wgrad_f32<R>>(smem);
+  if (e != cudaSuccess) return e;
   // by both widths, so that a gradient does not depend on whether the other is asked for
-  const int cluster = lora_token_split(a.plan.T, ka + nb, kTok);
+  const int cluster = lora_token_split(a.plan.T, ka + nb, kTok, wgrad_per_sm<R>());
   return launch_cluster_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, smem, s,
                             a, ba);
 }

@@ -7,28 +7,37 @@
 
 namespace rdfft {
 
-// Tile list of the low-rank rows kernels (adapter_plan.h): tiles of 64 tokens once the mean
-// group has 32, else of 16. A tile reads its adapter's A and B once, so longer tiles read them
-// less often; a group far below 64 would leave most of a tile's rows empty.
-inline int lora_list(int64_t T, int n) { return T >= 32 * (int64_t)n ? 2 : 1; }
+// Tile list of the low-rank rows kernels (adapter_plan.h): tiles of 64 tokens (list 2) from
+// T = 1024 on while the mean group has 32, else of 16 (list 1). A tile reads its adapter's A and
+// B once, so longer tiles read them less often; short batches lack tiles to fill the SMs, and a
+// group far below 64 leaves most of a tile's rows empty. bf16, K = N = 4096, r = 64, 4 adapters,
+// tiles of 16 against 64: T = 777 22.4 and 28.6 us, T = 1500 36.4 and 30.1; fp32, K = N = 2048,
+// r = 16: T = 777 17.9 and 23.2, T = 1500 24.9 and 25.4, T = 4096 52.5 and 41.6.
+inline int lora_list(int64_t T, int n) { return T >= 1024 && T >= 32 * (int64_t)n ? 2 : 1; }
 
-// CTAs per cluster (per tile) of the low-rank rows kernels: 8 while the tiles are few, so
-// that a tile's columns spread over more SMs, fewer when narrow rows would leave a CTA less
-// than 256 columns (one step of its 8 warps).
-inline int lora_cluster(int64_t tiles, int K, int N) {
-  int c = tiles <= 64 ? 8 : 4;
+// CTAs per cluster (per tile) of the low-rank rows kernels: as many as let the clusters start
+// together (a cluster's CTAs take separate SMs of one GPC), so that a tile's columns spread
+// over more SMs, and not so many that a CTA has less than 256 columns (fp32: 64). A 64-token tile of bf16
+// has a long pipeline in each CTA and gains nothing from 8. bf16, r = 64 as above, 8, 4 and 2
+// CTAs: T = 16 12.1, 16.9, 27.8 us (2 tiles), T = 777 30.0, 22.4, 28.0 (52), T = 1500 44.9,
+// 41.7, 36.4 (97), T = 4096 63.7, 43.6, 52.4 (65 tiles of 64); fp32: T = 777 83.2, 75.7, 90.7,
+// T = 1500 88.5, 104.7, 196.9 (26 tiles of 64), T = 4096 217, 160, 200.
+inline int lora_cluster(int64_t tiles, int list, bool f32, int K, int N) {
+  int c;
+  if (list == 1) c = tiles <= (f32 ? 48 : 20) ? 8 : (tiles <= (f32 ? 150 : 56) ? 4 : 2);
+  else c = (f32 && tiles <= 40) ? 8 : (tiles <= 111 ? 4 : 2);
   const int widest = K > N ? K : N;
-  while (c > 1 && (int64_t)c * 256 > widest) c /= 2;
+  while (c > 1 && (int64_t)c * (f32 ? 64 : 256) > widest) c /= 2;
   return c;
 }
 
 // CTAs per cluster of the low-rank weight gradients, which share the batch's tokens: as many as
-// keep the grid of `blocks` clusters within about three CTAs per SM (one wave), at most 8, and
-// no more than the batch has pieces of `chunk` tokens.
-inline int lora_token_split(int64_t T, int blocks, int chunk) {
-  int64_t c = 444 / blocks;
-  const int64_t pieces = (T + chunk - 1) / chunk;
-  if (c > pieces) c = pieces;
+// keep the grid of `blocks` clusters within one wave of 148 x per_sm CTAs, at most 8, and no
+// more than the batch has tiles of `chunk` tokens.
+inline int lora_token_split(int64_t T, int blocks, int chunk, int per_sm) {
+  int64_t c = 148 * per_sm / blocks;
+  const int64_t tiles = (T + chunk - 1) / chunk;
+  if (c > tiles) c = tiles;
   return c < 1 ? 1 : (c > 8 ? 8 : (int)c);
 }
 
