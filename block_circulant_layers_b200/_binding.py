@@ -46,7 +46,7 @@ lib.adapter_plan.argtypes = [_vp, _i64, _int, _vp, _vp]
 lib.lora_fwd.argtypes = [_vp] * 8 + [_i64] + [_int] * 5 + [_vp]
 lib.lora_bwd.argtypes = [_vp] * 11 + [_i64] + [_int] * 5 + [_vp]
 lib.circ_fwd_many.argtypes = [_vp] * 5 + [_i64] + [_int] * 4 + [_vp]
-lib.circ_bwd_many_workspace_size.argtypes = [_i64] + [_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
+lib.circ_bwd_many_workspace_size.argtypes = [_i64] + [_int] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
 lib.circ_bwd_many.argtypes = [_vp] * 6 + [_i64] + [_int] * 4 + [_vp, ctypes.c_size_t, _vp]
 lib.grad_norm_workspace_size.argtypes = [_int, ctypes.POINTER(ctypes.c_size_t)]
 lib.grad_norm.argtypes = [_vp, _vp, _vp, _int, _vp, _vp, ctypes.c_size_t, _vp]

@@ -28,6 +28,7 @@
 
 #include "bulk_copy.cuh"
 #include "circ_kernels.cuh"
+#include "circ_many.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -52,42 +53,62 @@ struct FusedSmem {
   static constexpr size_t BYTES = MBAR_OFF + (STG ? 16 : 0);
 };
 
-// QJ: the input blocks j of a CTA group (blockIdx.y): the CTA transforms g in full but x
-// only for its group's blocks, keeps the cross-spectrum S_ij of its group (every i) and
-// forms grad_x for its group's blocks. QJ = q for layers with few blocks; at q = 32 (p = 128)
-// four groups keep each CTA's part within tensor memory, and g is transformed once per group
-// (4 times a token, against 6 times for the separate grad_x and grad_c kernels).
-template <int P, int Q, int QJ, typename T, int NT, int TT, int RI, int RJ>
-__global__ void __launch_bounds__(NT, 1)
-k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
-                 T* __restrict__ grad_x, float* __restrict__ grad_c, float* __restrict__ partial, int64_t B,
-                 int64_t tok_per_cta) {
+// Shape constants of one instance.
+template <int P, int Q, int QJ, int NT, int RI, int RJ>
+struct FusedShape {
+  static constexpr int HB = P / 2;
+  static constexpr int RJP = RJ / 2;
+  static constexpr int ACC = RI * RJ * 2;           // floats of cross-spectrum per thread
+  static constexpr int NS = QJ * HB / NT;           // grad_x output blocks per thread (one bin)
+  static constexpr int CPI = 2 * NS;                // c_hat floats per thread and summed block i
+  static constexpr int BPL = 16 / CPI;              // summed blocks per 16-column tensor-memory load
+  static constexpr int CH = CPI * Q;                // floats of c_hat per thread
+  static constexpr int PER = ACC + CH;              // tensor-memory columns per thread
+  static constexpr int WQ = NT / 128;               // warps per tensor-memory lane quarter
+  static constexpr int COLS = WQ * PER;
+};
+
+// The rows of the tile of positions [tk, tk + TT) into the staging buffer (thread 0). `rows`
+// gives the activation row of a position.
+template <int P, int Q, int QJ, typename T, int TT, typename Rows>
+__device__ __forceinline__ void fused_fill(float* tile, const T* g, const T* x, const Rows& rows, int64_t tk,
+                                           int64_t tend, int j0) {
+  using SM = FusedSmem<P, Q, QJ, T, TT>;
+  constexpr int D = Q * P;
+  T* stage = reinterpret_cast<T*>(tile + SM::TILE_WORDS);
+  uint64_t* mbar = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(tile) + SM::MBAR_OFF);
+  const int nt = (int)((tend - tk) < TT ? (tend - tk) : TT);
+  mbar_arrive_expect_tx(mbar, (unsigned)(nt * (D + QJ * P) * (int)sizeof(T)));
+  for (int t = 0; t < nt; ++t) {
+    const int64_t row = rows.row(tk + t);
+    bulk_load(stage + (size_t)t * D, g + row * (int64_t)D, (unsigned)(D * sizeof(T)), mbar);
+    bulk_load(stage + SM::STAGE_G + (size_t)t * QJ * P, x + row * (int64_t)D + (int64_t)j0 * P,
+              (unsigned)(QJ * P * sizeof(T)), mbar);
+  }
+}
+
+// The tokens at positions [tbeg, tend) of one layer (one c_hat): grad_x of each, and the
+// packed cross-spectrum of all into gc_base (stored, or added to it). The caller has set up
+// tensor memory (tmem, its base) and, when staging, the mbarrier (`phase` its next parity);
+// with `prefilled` the first tile's rows are already requested. False when a wait gave up.
+template <int P, int Q, int QJ, typename T, int NT, int TT, int RI, int RJ, typename Rows>
+__device__ __forceinline__ bool fused_segment(const T* __restrict__ g, const T* __restrict__ x,
+                                              const float* __restrict__ chat, T* __restrict__ grad_x,
+                                              float* __restrict__ gc_base, bool store, const Rows& rows,
+                                              int64_t tbeg, int64_t tend, uint32_t tmem, unsigned& phase,
+                                              bool prefilled) {
   using G = LayerGeo<P>;
+  using F = FusedShape<P, Q, QJ, NT, RI, RJ>;
   constexpr int q = Q;
-  constexpr int HB = P / 2;
-  constexpr int RJP = RJ / 2;
-  constexpr int ACC = RI * RJ * 2;                  // floats of cross-spectrum per thread
-  constexpr int NS = QJ * HB / NT;                  // grad_x output blocks per thread (one bin)
-  constexpr int CPI = 2 * NS;                       // c_hat floats per thread and summed block i
-  constexpr int BPL = 16 / CPI;                     // summed blocks per 16-column tensor-memory load
-  constexpr int CH = CPI * Q;                       // floats of c_hat per thread
-  constexpr int PER = ACC + CH;                     // tensor-memory columns per thread
-  constexpr int WQ = NT / 128;                      // warps per tensor-memory lane quarter
-  constexpr int COLS = WQ * PER;
+  constexpr int HB = F::HB, RJP = F::RJP, ACC = F::ACC, NS = F::NS, CPI = F::CPI, BPL = F::BPL, CH = F::CH,
+                PER = F::PER, COLS = F::COLS;
   static_assert(RJ % 2 == 0 && ACC % 16 == 0 && CH % 16 == 0, "accumulator layout");
   static_assert((COLS & (COLS - 1)) == 0 && COLS >= 32 && COLS <= 512, "tensor-memory allocation");
   static_assert(NT % HB == 0 && NS >= 1, "the grad_x slots of a thread share one bin");
   static_assert(Q % QJ == 0 && QJ % RJ == 0 && 16 % CPI == 0 && Q % BPL == 0, "block groups");
   static_assert(NS % 2 == 0 || (NS == 1 && TT % 2 == 0), "slot pairs, or token pairs for one slot");
   extern __shared__ float tile[];
-  __shared__ uint32_t tmem_holder;
   const int D = q * P;
-  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
-  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
-  // one token slice stores its sums (they are final); with per-slice sums (partial) every
-  // slice stores its own q x q x p spectrum the same way; otherwise the slices add
-  const bool store = (gridDim.x == 1) || partial != nullptr;
-  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * q * q * P : grad_c;
   const int warp = threadIdx.x >> 5;
   const int j0 = blockIdx.y * QJ;                   // the group's first input block
   const int nib = q / RI;
@@ -96,29 +117,11 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
   using SM = FusedSmem<P, Q, QJ, T, TT>;
   T* stage = reinterpret_cast<T*>(tile + SM::TILE_WORDS);
   uint64_t* mbar = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(tile) + SM::MBAR_OFF);
-  // the rows of the tile starting at token tk into the staging buffer (thread 0)
-  auto fill = [&](int64_t tk) {
-    const int nt = (int)((tend - tk) < TT ? (tend - tk) : TT);
-    mbar_arrive_expect_tx(mbar, (unsigned)(nt * (D + QJ * P) * (int)sizeof(T)));
-    for (int t = 0; t < nt; ++t) {
-      bulk_load(stage + (size_t)t * D, g + (tk + t) * (int64_t)D, (unsigned)(D * sizeof(T)), mbar);
-      bulk_load(stage + SM::STAGE_G + (size_t)t * QJ * P, x + (tk + t) * (int64_t)D + (int64_t)j0 * P,
-                (unsigned)(QJ * P * sizeof(T)), mbar);
-    }
-  };
-
-  griddep_wait();
+  auto fill = [&](int64_t tk) { fused_fill<P, Q, QJ, T, TT>(tile, g, x, rows, tk, tend, j0); };
   if constexpr (SM::STG) {
-    if (threadIdx.x == 0) {
-      mbar_init(mbar, 1);
-      if (tbeg < tend) fill(tbeg);
-    }
+    if (!prefilled && threadIdx.x == 0) fill(tbeg);
   }
-  if (warp == 0) tc::tmem_alloc(&tmem_holder, COLS);
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tacc = tmem_holder + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(PER * (warp >> 2));
+  const uint32_t tacc = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(PER * (warp >> 2));
   const uint32_t tch = tacc + ACC;
   float acc[ACC];
 #pragma unroll
@@ -158,7 +161,6 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
   tc::tmem_wait_st();
 
   bool failed = false;
-  unsigned phase = 0;
   for (int64_t tok0 = tbeg; tok0 < tend; tok0 += TT) {
     const int ntok = (int)((tend - tok0) < TT ? (tend - tok0) : TT);
     if (tok0 != tbeg) __syncthreads();              // the previous tile is fully consumed
@@ -177,12 +179,12 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
       if (r < XR) {
         const int t = r / q, b = r - t * q;
         if (t >= ntok) return nullptr;
-        return SM::STG ? stage + (size_t)t * D + (size_t)b * P : g + (tok0 + t) * (int64_t)D + (int64_t)b * P;
+        return SM::STG ? stage + (size_t)t * D + (size_t)b * P : g + rows.row(tok0 + t) * (int64_t)D + (int64_t)b * P;
       }
       const int t = (r - XR) / QJ, jl = r - XR - t * QJ;
       if (t >= ntok) return nullptr;
       return SM::STG ? stage + SM::STAGE_G + (size_t)(t * QJ + jl) * P
-                     : x + (tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
+                     : x + rows.row(tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
     };
     // only the rows of the tile's ntok tokens are transformed: the r-th is g row r for
     // r < ntok q, then x row XR + (r - ntok q), so a partial last tile takes fewer rounds
@@ -369,7 +371,7 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
     // 4. rdIFFT (Hartley form) of the grad_x rows straight to HBM
     ifft_rows_mirrored<P, NT, T>(tile + G::row_base(XR), ntok * QJ, [&](int r) -> T* {
       const int t = r / QJ, jl = r - t * QJ;
-      return grad_x + (tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
+      return grad_x + rows.row(tok0 + t) * (int64_t)D + (int64_t)(j0 + jl) * P;
     });
   }
 
@@ -396,6 +398,83 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
         }
       }
   }
+  return !failed;
+}
+
+// QJ: the input blocks j of a CTA group (blockIdx.y): the CTA transforms g in full but x
+// only for its group's blocks, keeps the cross-spectrum S_ij of its group (every i) and
+// forms grad_x for its group's blocks. QJ = q for layers with few blocks; at q = 32 (p = 128)
+// four groups keep each CTA's part within tensor memory, and g is transformed once per group
+// (4 times a token, against 6 times for the separate grad_x and grad_c kernels).
+template <int P, int Q, int QJ, typename T, int NT, int TT, int RI, int RJ>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
+                 T* __restrict__ grad_x, float* __restrict__ grad_c, float* __restrict__ partial, int64_t B,
+                 int64_t tok_per_cta) {
+  using SM = FusedSmem<P, Q, QJ, T, TT>;
+  constexpr int COLS = FusedShape<P, Q, QJ, NT, RI, RJ>::COLS;
+  extern __shared__ float tile[];
+  __shared__ uint32_t tmem_holder;
+  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
+  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
+  // one token slice stores its sums (they are final); with per-slice sums (partial) every
+  // slice stores its own q x q x p spectrum the same way; otherwise the slices add
+  const bool store = (gridDim.x == 1) || partial != nullptr;
+  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * Q * Q * P : grad_c;
+  const int warp = threadIdx.x >> 5;
+  const DensePositions rows;
+  griddep_wait();
+  if constexpr (SM::STG) {
+    if (threadIdx.x == 0) {
+      mbar_init(reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(tile) + SM::MBAR_OFF), 1);
+      if (tbeg < tend) fused_fill<P, Q, QJ, T, TT>(tile, g, x, rows, tbeg, tend, blockIdx.y * QJ);
+    }
+  }
+  if (warp == 0) tc::tmem_alloc(&tmem_holder, COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  unsigned phase = 0;
+  fused_segment<P, Q, QJ, T, NT, TT, RI, RJ>(g, x, chat, grad_x, gc_base, store, rows, tbeg, tend, tmem_holder, phase,
+                                             true);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tmem_holder, COLS);
+}
+
+// The same for a batch of n adapters (circ_many.cuh): slice blockIdx.x takes an equal part of
+// the sorted positions that have an adapter, adapter by adapter, and stores each one's sums in
+// slot (slice + adapter) of `slots`, which no other slice and adapter share.
+template <int P, int Q, int QJ, typename T, int NT, int TT, int RI, int RJ>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_many_fused(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
+                  T* __restrict__ grad_x, float* __restrict__ slots, PlanView plan) {
+  using SM = FusedSmem<P, Q, QJ, T, TT>;
+  constexpr int COLS = FusedShape<P, Q, QJ, NT, RI, RJ>::COLS;
+  extern __shared__ float tile[];
+  __shared__ uint32_t tmem_holder;
+  const int warp = threadIdx.x >> 5;
+  griddep_wait();
+  if (!plan_matches(plan)) return;
+  if constexpr (SM::STG) {
+    if (threadIdx.x == 0)
+      mbar_init(reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(tile) + SM::MBAR_OFF), 1);
+  }
+  if (warp == 0) tc::tmem_alloc(&tmem_holder, COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const PlannedPositions rows{plan.order};
+  SliceWalk walk(plan);
+  unsigned phase = 0;
+  while (walk.next(plan)) {
+    if (!fused_segment<P, Q, QJ, T, NT, TT, RI, RJ>(
+            g, x, chat + (int64_t)walk.ad * Q * Q * P, grad_x,
+            slots + ((int64_t)blockIdx.x + walk.ad) * Q * Q * P, true, rows, walk.beg, walk.end, tmem_holder, phase, false))
+      break;
+    __syncthreads();                                 // the segment's last tile and staging are consumed
+  }
+  zero_unplanned<P>(grad_x, plan, Q, blockIdx.y * QJ, QJ);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) tc::tmem_dealloc(tmem_holder, COLS);
@@ -433,11 +512,11 @@ cudaError_t run_fused(const void* g, const void* x, const float* chat, void* gra
 // the x rows, then the Hartley-form rdIFFT of those rows to HBM: 3 row transforms per token and
 // block against 2 + 2 for the two kernels. Bin 0 holds the real pair (y_0, y_{p/2}), whose
 // products are component-wise.
-template <int P, int Q, typename T, int NT, int TT>
-__global__ void __launch_bounds__(NT, 1)
-k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
-                 T* __restrict__ grad_x, float* __restrict__ grad_c, float* __restrict__ partial, int64_t B,
-                 int64_t tok_per_cta) {
+template <int P, int Q, typename T, int NT, int TT, typename Rows>
+__device__ __forceinline__ void small_segment(const T* __restrict__ g, const T* __restrict__ x,
+                                              const float* __restrict__ chat, T* __restrict__ grad_x,
+                                              float* __restrict__ gc_base, bool store, const Rows& rows,
+                                              int64_t tbeg, int64_t tend) {
   using G = LayerGeo<P>;
   constexpr int HB = P / 2;
   constexpr int KB = (HB + NT - 1) / NT;            // bins per thread: k = tid + NT u
@@ -445,11 +524,6 @@ k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* 
   constexpr int D = Q * P;
   static_assert(NT % G::TPR == 0 && (G::RW == 1 || XR % G::RW == 0), "whole rows; additive row bases");
   extern __shared__ float tile[];
-  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
-  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
-  const bool store = (gridDim.x == 1) || partial != nullptr;   // as in k_circ_bwd_fused
-  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * Q * Q * P : grad_c;
-  griddep_wait();
 
   float sr[KB][Q][Q], si[KB][Q][Q], cr[KB][Q][Q], ci[KB][Q][Q];
 #pragma unroll
@@ -474,7 +548,7 @@ k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* 
       const int rr = isx ? r - XR : r;
       const int t = rr / Q, b = rr - t * Q;
       if (t >= ntok) return nullptr;
-      return (isx ? x : g) + (tok0 + t) * (int64_t)D + (int64_t)b * P;
+      return (isx ? x : g) + rows.row(tok0 + t) * (int64_t)D + (int64_t)b * P;
     });
     __syncthreads();
     // 2. per bin: S_ij += G_i conj(X_j); Y_j = sum_i conj(C_ij) G_i over the x rows (mirrored:
@@ -523,7 +597,7 @@ k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* 
     // 3. rdIFFT (Hartley form) of the grad_x rows straight to HBM
     ifft_rows_mirrored<P, NT, T>(tile + G::row_base(XR), XR, [&](int r) -> T* {
       const int t = r / Q, j = r - t * Q;
-      return t < ntok ? grad_x + (tok0 + t) * (int64_t)D + (int64_t)j * P : nullptr;
+      return t < ntok ? grad_x + rows.row(tok0 + t) * (int64_t)D + (int64_t)j * P : nullptr;
     });
   }
   // 4. the CTA's cross-spectrum into grad_c (row i q + j)
@@ -550,6 +624,36 @@ k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* 
 }
 
 template <int P, int Q, typename T, int NT, int TT>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
+                 T* __restrict__ grad_x, float* __restrict__ grad_c, float* __restrict__ partial, int64_t B,
+                 int64_t tok_per_cta) {
+  const int64_t tbeg = (int64_t)blockIdx.x * tok_per_cta;
+  const int64_t tend = (tbeg + tok_per_cta < B) ? tbeg + tok_per_cta : B;
+  const bool store = (gridDim.x == 1) || partial != nullptr;   // as in k_circ_bwd_fused
+  float* const gc_base = partial != nullptr ? partial + (int64_t)blockIdx.x * Q * Q * P : grad_c;
+  griddep_wait();
+  small_segment<P, Q, T, NT, TT>(g, x, chat, grad_x, gc_base, store, DensePositions(), tbeg, tend);
+}
+
+// As k_circ_many_fused.
+template <int P, int Q, typename T, int NT, int TT>
+__global__ void __launch_bounds__(NT, 1)
+k_circ_many_small(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
+                  T* __restrict__ grad_x, float* __restrict__ slots, PlanView plan) {
+  griddep_wait();
+  if (!plan_matches(plan)) return;
+  const PlannedPositions rows{plan.order};
+  SliceWalk walk(plan);
+  while (walk.next(plan)) {
+    small_segment<P, Q, T, NT, TT>(g, x, chat + (int64_t)walk.ad * Q * Q * P, grad_x,
+                                   slots + ((int64_t)blockIdx.x + walk.ad) * Q * Q * P, true, rows, walk.beg, walk.end);
+    __syncthreads();                                 // the segment's last tile is consumed
+  }
+  zero_unplanned<P>(grad_x, plan, Q, 0, Q);
+}
+
+template <int P, int Q, typename T, int NT, int TT>
 cudaError_t run_small(const void* g, const void* x, const float* chat, void* grad_x, float* grad_c, int64_t B,
                       cudaStream_t s, GcSink* sink) {
   auto kern = k_circ_bwd_small<P, Q, T, NT, TT>;
@@ -568,6 +672,71 @@ cudaError_t run_small(const void* g, const void* x, const float* chat, void* gra
   return launch_pdl(kern, dim3((unsigned)slices), dim3(NT), smem, s, static_cast<const T*>(g),
                     static_cast<const T*>(x), chat, static_cast<T*>(grad_x), grad_c, partial, B,
                     (int64_t)(tiles_per * TT));
+}
+
+template <int P, int Q, int QJ, typename T, int TT, int RI, int RJ>
+cudaError_t run_many_fused(const CircMany& a, const void* g, void* grad_x, cudaStream_t s, GcSink* sink) {
+  constexpr int NT = 512, NJG = Q / QJ;
+  auto kern = k_circ_many_fused<P, Q, QJ, T, NT, TT, RI, RJ>;
+  const size_t smem = FusedSmem<P, Q, QJ, T, TT>::BYTES;
+  const int slices = circ_many_slices(a.T, a.n, NJG, TT, num_sms());
+  if (!many_slots(sink, slices, a, (int64_t)Q * Q * P)) return cudaSuccess;
+  const cudaError_t e = set_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)slices, (unsigned)NJG), dim3(NT), smem, s, static_cast<const T*>(g),
+                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), sink->partial,
+                    plan_view(a.plan, a.T, a.n, 0));
+}
+
+template <int P, int Q, typename T, int NT, int TT>
+cudaError_t run_many_small(const CircMany& a, const void* g, void* grad_x, cudaStream_t s, GcSink* sink) {
+  auto kern = k_circ_many_small<P, Q, T, NT, TT>;
+  const size_t smem = sizeof(float) * (size_t)LayerGeo<P>::words(2 * TT * Q);
+  const int slices = circ_many_slices(a.T, a.n, 1, TT, num_sms());
+  if (!many_slots(sink, slices, a, (int64_t)Q * Q * P)) return cudaSuccess;
+  const cudaError_t e = set_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)slices), dim3(NT), smem, s, static_cast<const T*>(g),
+                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), sink->partial,
+                    plan_view(a.plan, a.T, a.n, 0));
+}
+
+// The instances of fused_t, over a plan.
+template <typename T>
+cudaError_t many_fused_t(const CircMany& a, const void* g, void* grad_x, int p, cudaStream_t s, GcSink* sink) {
+  const int q = a.D / p;
+  if (q == 1) {
+    switch (p) {
+      case 512: return run_many_small<512, 1, T, 128, 4>(a, g, grad_x, s, sink);
+      case 1024: return run_many_small<1024, 1, T, 128, 2>(a, g, grad_x, s, sink);
+      case 2048: return run_many_small<2048, 1, T, 256, 2>(a, g, grad_x, s, sink);
+      case 4096: return run_many_small<4096, 1, T, 512, 2>(a, g, grad_x, s, sink);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+  if (q == 2) {
+    switch (p) {
+      case 512: return run_many_small<512, 2, T, 128, 2>(a, g, grad_x, s, sink);
+      case 1024: return run_many_small<1024, 2, T, 256, 2>(a, g, grad_x, s, sink);
+      case 2048: return run_many_small<2048, 2, T, 512, 2>(a, g, grad_x, s, sink);
+      case 4096: return run_many_small<4096, 2, T, 512, 1>(a, g, grad_x, s, sink);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+  const int nsm = num_sms();
+  if (p == 128 && q == 32) {
+    if (layer_fused_small_tiles(a.T, 2, 4, nsm)) return run_many_fused<128, 32, 8, T, 2, 4, 8>(a, g, grad_x, s, sink);
+    return run_many_fused<128, 32, 8, T, 4, 4, 8>(a, g, grad_x, s, sink);
+  }
+  if (p == 512 && q == 8) {
+    if (layer_fused_small_tiles(a.T, 2, 1, nsm)) return run_many_fused<512, 8, 8, T, 2, 4, 8>(a, g, grad_x, s, sink);
+    return run_many_fused<512, 8, 8, T, 4, 4, 8>(a, g, grad_x, s, sink);
+  }
+  if (p == 1024 && q == 4) {
+    if (layer_fused_small_tiles(a.T, 1, 1, nsm)) return run_many_fused<1024, 4, 4, T, 1, 4, 4>(a, g, grad_x, s, sink);
+    return run_many_fused<1024, 4, 4, T, 2, 4, 4>(a, g, grad_x, s, sink);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>
@@ -632,6 +801,13 @@ bool circ_bwd_fused_supported(int p, int D, int64_t B) {
   return (p == 512 && D == 4096) || (p == 1024 && D == 4096) || (p == 128 && D == 4096) ||
          ((D == p || D == 2 * p) && p >= 512);
 }
+
+cudaError_t launch_circ_many_fused(const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink) {
+  if (dtype == 0) return many_fused_t<float>(a, a.g, a.out, p, s, sink);
+  return many_fused_t<bf16_t>(a, a.g, a.out, p, s, sink);
+}
+
+cudaError_t take_many_fused_plan_error(unsigned int* flags) { return take_error_word(flags); }
 
 cudaError_t launch_circ_bwd_fused(const void* g, const void* x, const float* chat, void* grad_x, float* grad_c,
                                   int64_t B, int D, int p, int dtype, cudaStream_t s, GcSink* sink) {

@@ -90,14 +90,6 @@ static cudaError_t launch_sum_slices(const float* part, int slices, int64_t n, f
                     reinterpret_cast<const float4*>(part), n4, slices, reinterpret_cast<float4*>(out));
 }
 
-cudaError_t finish_grad_c(const GcSink& sink, float* grad_c, int64_t rows, int p, cudaStream_t s) {
-  cudaError_t r = cudaSuccess;
-  if (sink.partial != nullptr && sink.slices > 1)
-    r = launch_sum_slices(sink.partial, sink.slices, rows * p, grad_c, s);
-  if (r == cudaSuccess && !sink.ifft_done) r = launch_rows(grad_c, rows, p, 0, true, s);
-  return r;
-}
-
 cudaError_t launch_circ_bwd(const void* g, const void* x, const float* c_hat, void* grad_x,
                             float* grad_c, int64_t B, int D, int p, int dtype, cudaStream_t s, GcSink* sink) {
   const int q = D / p;
@@ -105,9 +97,11 @@ cudaError_t launch_circ_bwd(const void* g, const void* x, const float* c_hat, vo
   // after the grad_c kernel: the ordered sum of the slices (deterministic mode), then the
   // in-place rdIFFT unless the kernel ran it itself
   auto finish_gc = [&](bool ifft_done) -> cudaError_t {
-    GcSink done = sink != nullptr ? *sink : GcSink();
-    done.ifft_done = ifft_done;
-    return finish_grad_c(done, grad_c, (int64_t)q * q, p, s);
+    cudaError_t r = cudaSuccess;
+    if (sink != nullptr && sink->partial != nullptr && sink->slices > 1)
+      r = launch_sum_slices(sink->partial, sink->slices, (int64_t)q * q * p, grad_c, s);
+    if (r == cudaSuccess && !ifft_done) r = launch_rows(grad_c, (int64_t)q * q, p, 0, true, s);
+    return r;
   };
   if (grad_c != nullptr && grad_x != nullptr && circ_bwd_fused_supported(p, D, B)) {
     // both gradients from one transform of g and x (circ_bwd_fused.cu), then grad_c's rdIFFT

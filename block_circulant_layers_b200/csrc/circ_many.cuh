@@ -26,16 +26,21 @@ struct PlannedPositions {
   __device__ __forceinline__ int64_t row(int64_t pos) const { return __ldg(order + pos); }
 };
 
+// Requests `bytes` (a multiple of 16, as is the address) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 template <int P, typename T, int NT, int TT, int NS, bool BWDX>
 __global__ void __launch_bounds__(NT, NT >= 512 ? 1 : (NT >= 256 ? 2 : 1))
 k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T* base, T* out, int q, int QI,
-              PlanView plan, const int* __restrict__ group) {
+              PlanView plan) {
   griddep_wait();
   if (!plan_matches(plan)) return;
   int pos, ad, m;
   if constexpr (TT == 1) {
     pos = blockIdx.x;                                       // one token per CTA: no tile list
-    ad = __ldg(group + pos);
+    ad = __ldg(plan.group + pos);
     m = 1;
   } else {
     static_assert(TT == 2 || TT == 4, "a CTA takes a whole tile of the 4-token list, or half of it");
@@ -48,6 +53,9 @@ k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T*
   }
   const int o0 = blockIdx.y * QI, D = q * P;
   PlannedTokens tok{plan.order + pos, m};
+  // the base rows are added at the very end: into L2 meanwhile
+  if (base != nullptr && ad < plan.n && threadIdx.x < m)
+    prefetch_l2(base + tok.row(threadIdx.x) * (int64_t)D + (int64_t)o0 * P, QI * P * (int)sizeof(T));
   if (ad >= plan.n) {                                       // no adapter: the base row, or zeros
     if (base == out) return;
     for (int e = threadIdx.x; e < m * QI * P; e += NT) {
@@ -63,20 +71,63 @@ k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T*
   });
 }
 
-// grid: token slices x input-block groups x adapters. Slice s of adapter a sums an equal part
-// of the adapter's tokens (whole tiles) into its own q x q x p spectrum.
+// Token slices of the gradient kernels: slice blockIdx.x takes an equal part of the sorted
+// positions that have an adapter, and walks it adapter by adapter (a part per adapter would
+// leave the launch to the adapter with most tokens). No slice is empty but those beyond the
+// number of tokens, so every slot that k_sum_slots reads has been written.
+struct SliceWalk {
+  int64_t pos, hi, beg, end;                                // [beg, end): tokens of adapter ad
+  int ad;
+  __device__ __forceinline__ explicit SliceWalk(const PlanView& v) {
+    const int64_t tokens = __ldg(v.offsets + v.n);
+    const int64_t slices = min((int64_t)gridDim.x, tokens);
+    pos = hi = 0;
+    if (blockIdx.x < slices) {
+      pos = tokens * blockIdx.x / slices;
+      hi = tokens * (blockIdx.x + 1) / slices;
+    }
+    beg = end = pos;
+    ad = 0;
+  }
+  __device__ __forceinline__ bool next(const PlanView& v) {
+    if (pos >= hi) return false;
+    ad = __ldg(v.group + pos);
+    beg = pos;
+    end = min((int64_t)__ldg(v.offsets + ad + 1), hi);
+    pos = end;
+    return true;
+  }
+};
+
+// grad_x of the tokens without an adapter: zeros in blocks [j0, j0 + QJ), shared by the slices.
+template <int P, typename T>
+__device__ __forceinline__ void zero_unplanned(T* grad_x, const PlanView& v, int q, int j0, int QJ) {
+  const int beg = __ldg(v.offsets + v.n), end = __ldg(v.offsets + v.n + 1), w = QJ * P;
+  for (int t = beg + blockIdx.x; t < end; t += gridDim.x)
+    for (int e = threadIdx.x; e < w; e += blockDim.x)
+      grad_x[(int64_t)__ldg(v.order + t) * q * P + (int64_t)j0 * P + e] = from_f32<T>(0.0f);
+}
+
+// grid: token slices x input-block groups. The sums of slice s over adapter a go to slot s + a
+// of `slots`: in the order of the positions, each next pair has a larger s, a or both.
 template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
 __global__ void __launch_bounds__(NT, 1)
-k_circ_many_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ sums, int q, int QJ,
-               PlanView plan, int ifft_here) {
+k_circ_many_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ slots, int q, int QJ,
+               PlanView plan) {
   griddep_wait();
   if (!plan_matches(plan)) return;
-  const int ad = blockIdx.z;
-  const int64_t beg = __ldg(plan.offsets + ad), end = __ldg(plan.offsets + ad + 1);
-  const int64_t tiles = (end - beg + TT - 1) / TT, per = (tiles + gridDim.x - 1) / gridDim.x * TT;
-  const int64_t tbeg = min(beg + (int64_t)blockIdx.x * per, end), tend = min(tbeg + per, end);
-  float* const gc = sums + ((int64_t)blockIdx.x * plan.n + ad) * q * q * P;
-  circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, gc, PlannedPositions{plan.order}, tbeg, tend, q, QJ, true, ifft_here);
+  SliceWalk walk(plan);
+  while (walk.next(plan)) {
+    circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, slots + ((int64_t)blockIdx.x + walk.ad) * q * q * P,
+                                           PlannedPositions{plan.order}, walk.beg, walk.end, q, QJ, true, 0);
+    __syncthreads();                                        // the segment's last tile is consumed
+  }
+}
+
+// Records the slots of a launch in the sink; false when it was only to be planned.
+static inline bool many_slots(GcSink* sink, int slices, const CircMany& a, int64_t floats) {
+  sink->slices = slices;
+  return !sink->plan_only && (int64_t)(slices + a.n) * floats <= sink->partial_floats;
 }
 
 template <int P, typename T, int NT, int TT, int NS, bool BWDX>
@@ -93,7 +144,7 @@ static cudaError_t launch_many_x_cfg(const CircMany& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)gx, (unsigned)(q / QI)), dim3(NT), smem, s, static_cast<const T*>(a.in),
                     a.c_hat, static_cast<const T*>(a.base), static_cast<T*>(a.out), q, QI,
-                    plan_view(a.plan, a.T, a.n, 0), a.plan + lay.group);
+                    plan_view(a.plan, a.T, a.n, 0));
 }
 
 // The dense layer's shapes (launch_x_p), with the tokens per CTA bounded by the mean group.
@@ -130,17 +181,12 @@ static cudaError_t run_many_gc(const CircMany& a, int QJ, cudaStream_t s, GcSink
   const size_t smem = sizeof(float) * (size_t)LayerGeo<P>::words(TT * (q + QJ));
   const int njgroups = q / QJ;
   const int slices = circ_many_slices(a.T, a.n, njgroups, TT, num_sms());
-  const bool here = slices == 1 && (int64_t)q * QJ <= (int64_t)TT * (q + QJ);
-  float* partial = nullptr;
-  cudaError_t e = sink_plan(sink, slices, (int64_t)a.n * q * q * P, &partial);
-  sink->ifft_done = here;
-  if (e != cudaSuccess || sink->plan_only) return e;
-  if (slices > 1 && partial == nullptr) return cudaErrorInvalidValue;
-  e = set_smem(kern, smem);
+  if (!many_slots(sink, slices, a, (int64_t)q * q * P)) return cudaSuccess;
+  const cudaError_t e = set_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)slices, (unsigned)njgroups, (unsigned)a.n), dim3(NT), smem, s,
-                    static_cast<const T*>(a.g), static_cast<const T*>(a.in), partial ? partial : a.grad_c, q, QJ,
-                    plan_view(a.plan, a.T, a.n, 0), here ? 1 : 0);
+  return launch_pdl(kern, dim3((unsigned)slices, (unsigned)njgroups), dim3(NT), smem, s,
+                    static_cast<const T*>(a.g), static_cast<const T*>(a.in), sink->partial, q, QJ,
+                    plan_view(a.plan, a.T, a.n, 0));
 }
 
 // Accumulator shapes as launch_gc_tt.
@@ -171,7 +217,7 @@ static cudaError_t launch_many_gc_p(const CircMany& a, cudaStream_t s, GcSink* s
   return run_many_gc<P, T, NT, TT, 32, 1, 1>(a, QJ, s, sink);
 }
 
-// op 0 = forward (in = x), 1 = grad_x (in = g), 2 = grad_c (g, in = x; see circ_layer_p).
+// op 0 = forward (in = x), 1 = grad_x (in = g), 2 = grad_c slots (g, in = x).
 template <int P>
 cudaError_t circ_many_p(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink) {
   if (dtype == 0) {

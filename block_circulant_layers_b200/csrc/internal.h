@@ -47,10 +47,6 @@ struct GcSink {
   bool ifft_done = false;        // out: the kernel also ran grad_c's rdIFFT (one slice)
 };
 
-// After a grad_c launch: the ordered sum of the slices, if the sink holds several, then the
-// in-place rdIFFT of grad_c's rows unless the kernel ran it itself.
-cudaError_t finish_grad_c(const GcSink& sink, float* grad_c, int64_t rows, int p, cudaStream_t s);
-
 // Backward in one kernel (grad_x and the grad_c cross-spectrum from one transform of g
 // and x per input-block group) for the shapes it covers (circ_bwd_fused_supported: D = 4096
 // at p = 128, 512 or 1024, and layers of one or two blocks, D in {p, 2p},
@@ -95,9 +91,13 @@ struct CircMany {
   int64_t T = 0;
   int D = 0, n = 0;
 };
-// op 0 = forward, 1 = grad_x, 2 = grad_c (the sink as in launch_circ_bwd; with several slices
-// its partial buffer is required, and plan_only fills in the slice count).
+// op 0 = forward, 1 = grad_x, 2 = grad_c's slots: per-slice sums in the sink's partial buffer,
+// (slices + n) x q x q x p floats; with plan_only the sink receives the slice count alone.
 cudaError_t launch_circ_many(int op, const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink);
+// grad_x (out) and grad_c's slots in one kernel, for the shapes of circ_bwd_fused_supported.
+cudaError_t launch_circ_many_fused(const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink);
+// The whole backward: grad_x if out, grad_c (spatial) if grad_c.
+cudaError_t launch_circ_many_bwd(const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink);
 
 // Low-rank adapters: rows (forward: in = x, w1 = a, w2 = b; bwd: in = g, w1 = b, w2 = a) and
 // weight gradients. Arguments as lora_fwd / lora_bwd in rdfft.h.

@@ -18,6 +18,7 @@ struct PlanView {
   const int* header;
   const int* offsets;
   const int* order;
+  const int* group;
   const int2* tiles;
   int list;
   int T, n;
@@ -29,6 +30,7 @@ inline PlanView plan_view(const int* plan, int64_t T, int n, int list) {
   v.header = plan;
   v.offsets = plan + l.offsets;
   v.order = plan + l.order;
+  v.group = plan + l.group;
   v.tiles = reinterpret_cast<const int2*>(plan + l.tiles[list]);
   v.list = list;
   v.T = (int)T;
@@ -111,7 +113,7 @@ struct TileShare {
 };
 
 // Asynchronous copies to shared memory.
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+__device__ __forceinline__ uint32_t shared_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 // 16 bytes to shared memory; zeros when !in (src is then not read, but must be a valid pointer).

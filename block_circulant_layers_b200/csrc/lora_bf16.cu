@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   constexpr int M = 64, COLS = S::kCols, UNITS = COLS / 8, ROWS = kThreads / UNITS, NH = M / ROWS;
   extern __shared__ __align__(128) unsigned char ring[];
   float* const part = reinterpret_cast<float*>(ring + S::kStage * S::kStages);     // [2][M][R]
-  const uint32_t ring_at = smem_addr(ring);
-  const uint32_t hi_at = smem_addr(part + 2 * M * R), lo_at = hi_at + M * R * 2;   // mid, tiles of R columns
+  const uint32_t ring_at = shared_at(ring);
+  const uint32_t hi_at = shared_at(part + 2 * M * R), lo_at = hi_at + M * R * 2;   // mid, tiles of R columns
   unsigned char* const mid_hi = reinterpret_cast<unsigned char*>(part + 2 * M * R);
   unsigned char* const mid_lo = mid_hi + M * R * 2;
 
@@ -584,7 +584,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   __shared__ __align__(16) int order[S::kOrders][S::kTok];
   unsigned char* const mid_p = ring + S::kStage * S::kStages;
   float* const head = reinterpret_cast<float*>(mid_p + S::kMid);   // [NA][kThreads]
-  const uint32_t ring_at = smem_addr(ring), mid_at = smem_addr(mid_p);
+  const uint32_t ring_at = shared_at(ring), mid_at = shared_at(mid_p);
   griddep_wait();
   if (!plan_matches(a.plan)) return;
   const unsigned C = cluster_size(), rank = cluster_rank();
@@ -638,7 +638,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
       if (i < count && tid < S::kTok) {
         const int pos = desc[i + 1].x + tid;
         const bool in = pos < desc[i + 2].x;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(&order[i % S::kOrders][tid])),
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_at(&order[i % S::kOrders][tid])),
                      "l"(in ? a.plan.order + pos : a.plan.order), "r"(in ? 4 : 0)
                      : "memory");
       }

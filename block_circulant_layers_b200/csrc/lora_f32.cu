@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   }
   auto request = [&](int step) {
     if (adapted && step < n1 + n2) {
-      const uint32_t dst = smem_addr(sm + step % S::kStages * S::kStage);
+      const uint32_t dst = shared_at(sm + step % S::kStages * S::kStage);
       if (step < n1) {
         const int k0 = kKC * (k_first + step);
 #pragma unroll

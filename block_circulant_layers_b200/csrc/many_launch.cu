@@ -22,10 +22,78 @@ cudaError_t launch_circ_many(int op, const CircMany& a, int p, int dtype, cudaSt
   }
 }
 
+// grad_c[a] = the slots of adapter a added in slice order: with S <= T' slices of T' planned tokens,
+// slice s holds positions [T' s / S, T' (s + 1) / S), and its sums over adapter a lie in slot
+// s + a. Zeros for an adapter without tokens. kSplit threads share an element, each adding
+// every kSplit-th slot, and their sums are added in order: the order depends on the plan alone.
+constexpr int kSumThreads = 256, kSplit = 8;
+
+__global__ void __launch_bounds__(kSumThreads) k_sum_slots(const float4* __restrict__ slots, int64_t n4, int slices,
+                                                           float4* __restrict__ out, PlanView plan) {
+  constexpr int EPB = kSumThreads / kSplit;
+  __shared__ float4 sums[kSplit][EPB];
+  griddep_wait();
+  if (!plan_matches(plan)) return;
+  const int ad = blockIdx.y, el = threadIdx.x % EPB, r = threadIdx.x / EPB;
+  const int64_t e = (int64_t)blockIdx.x * EPB + el;
+  const int64_t tokens = __ldg(plan.offsets + plan.n);
+  slices = (int)min((int64_t)slices, tokens);
+  const int beg = __ldg(plan.offsets + ad), end = __ldg(plan.offsets + ad + 1);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (e < n4 && beg < end) {
+    // the slice of a position: the last s with tokens s / slices <= position
+    const int first = (int)(((int64_t)(beg + 1) * slices - 1) / tokens), last = (int)(((int64_t)end * slices - 1) / tokens);
+#pragma unroll 4
+    for (int s = first + r; s <= last; s += kSplit) {
+      const float4 v = __ldcs(slots + (int64_t)(s + ad) * n4 + e);
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+  }
+  sums[r][el] = acc;
+  __syncthreads();
+  griddep_launch_dependents();
+  if (r == 0 && e < n4) {
+    float4 t = sums[0][el];
+#pragma unroll
+    for (int j = 1; j < kSplit; ++j) {
+      const float4 v = sums[j][el];
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+    out[(int64_t)ad * n4 + e] = t;
+  }
+}
+
+cudaError_t launch_circ_many_bwd(const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink) {
+  const int q = a.D / p;
+  const bool both = a.out != nullptr && a.grad_c != nullptr;
+  cudaError_t e = cudaSuccess;
+  if (a.grad_c != nullptr) {
+    e = both && circ_bwd_fused_supported(p, a.D, a.T) ? launch_circ_many_fused(a, p, dtype, s, sink)
+                                                      : launch_circ_many(2, a, p, dtype, s, sink);
+    if (e != cudaSuccess || sink->plan_only) return e;
+    const int64_t floats = (int64_t)q * q * p, n4 = floats / 4;
+    if ((int64_t)(sink->slices + a.n) * floats > sink->partial_floats) return cudaErrorInvalidValue;
+    constexpr int EPB = kSumThreads / kSplit;
+    e = launch_pdl(k_sum_slots, dim3((unsigned)((n4 + EPB - 1) / EPB), (unsigned)a.n), dim3(kSumThreads), 0, s,
+                   reinterpret_cast<const float4*>(sink->partial), n4, sink->slices,
+                   reinterpret_cast<float4*>(a.grad_c), plan_view(a.plan, a.T, a.n, 0));
+    if (e != cudaSuccess) return e;
+    e = launch_rows(a.grad_c, (int64_t)a.n * q * q, p, 0, true, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.out != nullptr && !(both && circ_bwd_fused_supported(p, a.D, a.T))) {
+    CircMany x = a;
+    x.in = a.g;
+    e = launch_circ_many(1, x, p, dtype, s, nullptr);
+  }
+  return e;
+}
+
 cudaError_t lora_rows_bf16(const LoraRows<bf16_t>& a, bool bwd, const int* plan, int64_t T, int n, cudaStream_t s);
 cudaError_t lora_rows_f32(const LoraRows<float>& a, bool bwd, const int* plan, int64_t T, int n, cudaStream_t s);
 cudaError_t lora_wgrad_bf16(const LoraWgrad<bf16_t>& a, cudaStream_t s);
 cudaError_t lora_wgrad_f32(const LoraWgrad<float>& a, cudaStream_t s);
+cudaError_t take_many_fused_plan_error(unsigned int* flags);
 cudaError_t take_lora_bf16_error(unsigned int* flags);
 cudaError_t take_lora_f32_error(unsigned int* flags);
 
@@ -77,6 +145,8 @@ cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, cons
 cudaError_t take_plan_device_error(unsigned int* flags) {
   *flags = 0;
   cudaError_t (*const words[])(unsigned int*) = {
+      take_error_word,
+      take_many_fused_plan_error,
       take_lora_bf16_error,
       take_lora_f32_error,
 #define RDFFT_MANY_WORD(PP) take_circ_many_error_##PP,

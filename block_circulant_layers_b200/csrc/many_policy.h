@@ -50,12 +50,12 @@ inline int circ_many_tokens(int64_t T, int n, int q, int qi_max, int n_sm, int t
   return layer_x_tokens(T, q, qi_max, n_sm, by_group < tt_max ? by_group : tt_max);
 }
 
-// Token slices per adapter of the grad_c kernel: about two CTAs per SM over njgroups groups of
-// n adapters (uneven groups then still spread), no more than the batch's tiles.
+// Token slices of the many-adapter gradient kernels: one CTA per SM over njgroups groups, no
+// more than the batch has token tiles (or adapters in use, a tile each, if those are more).
 inline int circ_many_slices(int64_t T, int n, int njgroups, int tt, int n_sm) {
-  const int64_t ctas = (int64_t)njgroups * n, tiles = (T + tt - 1) / tt;
-  int64_t s = 2 * n_sm / ctas;
-  if (s > tiles) s = tiles;
+  int64_t s = n_sm / njgroups;
+  const int64_t tiles = (T + tt - 1) / tt, used = T < n ? T : n, most = tiles > used ? tiles : used;
+  if (s > most) s = most;
   return s < 1 ? 1 : (int)s;
 }
 

@@ -189,7 +189,7 @@ py::tuple circ_bwd_many_(const Tensor& g, const Tensor& x, const Tensor& c_hat, 
   if (need_c) {
     gc = out_of(grad_c_, "grad_c", c_hat.sizes(), at::kFloat, x);
     size_t need = 0;
-    const int rc = circ_bwd_many_workspace_size(T, D, p, n, type, &need);
+    const int rc = circ_bwd_many_workspace_size(T, D, p, n, type, need_x, &need);
     if (rc != RDFFT_OK) return py::make_tuple(rc, py::none(), py::none());
     if (!ws && need) ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
   }

@@ -175,16 +175,6 @@ bool lora_sizes_ok(int64_t T, int K, int N, int r, int n) {
   return plan_sizes_ok(T, n) && width(K) && width(N) && r >= 8 && r <= 128 && r % 8 == 0;
 }
 
-int many_bwd_slices(int64_t T, int D, int p, int n, int dtype, int* slices) {
-  rdfft::CircMany a;
-  a.T = T, a.D = D, a.n = n;
-  rdfft::GcSink plan;
-  plan.plan_only = true;
-  const cudaError_t e = rdfft::launch_circ_many(2, a, p, dtype, nullptr, &plan);
-  *slices = plan.slices;
-  return finish(e);
-}
-
 // Argument checks shared by grad_norm and clip_grad_norm.
 int norm_args(const void* const* grads, const int64_t* numels, const int* dtypes, int count, float* norm,
               void* workspace, size_t workspace_bytes) {
@@ -453,16 +443,21 @@ int circ_fwd_many(const void* x, const float* c_hat, const void* base, void* y, 
   return finish(rdfft::launch_circ_many(0, c, p, dtype, reinterpret_cast<cudaStream_t>(stream), nullptr));
 }
 
-int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, size_t* bytes) {
+int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, int with_grad_x, size_t* bytes) {
   if (bytes == nullptr) return RDFFT_ENULL;
   *bytes = 0;
   if (!dtype_ok(dtype)) return RDFFT_EDTYPE;
   if (!layer_shape_ok(T, D, p) || !plan_sizes_ok(T, n)) return RDFFT_EINVAL;
   if (T == 0) return RDFFT_OK;
-  int slices = 0;
-  const int rc = many_bwd_slices(T, D, p, n, dtype, &slices);
-  if (rc == RDFFT_OK && slices > 1) *bytes = (size_t)slices * n * gc_bytes(D, p);
-  return rc;
+  rdfft::CircMany c;
+  c.T = T, c.D = D, c.n = n;
+  c.grad_c = reinterpret_cast<float*>(16);             // asked for; a plan touches no pointer
+  if (with_grad_x) c.out = c.grad_c;
+  rdfft::GcSink plan;
+  plan.plan_only = true;
+  const cudaError_t e = rdfft::launch_circ_many_bwd(c, p, dtype, nullptr, &plan);
+  if (e == cudaSuccess) *bytes = (size_t)(plan.slices + n) * gc_bytes(D, p);
+  return finish(e);
 }
 
 int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x, float* grad_c, const int32_t* plan,
@@ -481,9 +476,9 @@ int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x
   if (g == nullptr || plan == nullptr || (grad_x && c_hat == nullptr) || (grad_c && x == nullptr)) return RDFFT_ENULL;
   size_t need = 0;
   if (grad_c != nullptr) {
-    const int rc = circ_bwd_many_workspace_size(T, D, p, n, dtype, &need);
+    const int rc = circ_bwd_many_workspace_size(T, D, p, n, dtype, grad_x != nullptr, &need);
     if (rc != RDFFT_OK) return rc;
-    if (need > 0 && workspace == nullptr) return RDFFT_ENULL;
+    if (workspace == nullptr) return RDFFT_ENULL;
   }
   const size_t act = (size_t)T * D * (dtype == RDFFT_F32 ? 4 : 2);
   const Range args[] = {{grad_x, act}, {grad_c, cb}, {need ? workspace : nullptr, need}, {g, act}, {x, act},
@@ -492,22 +487,12 @@ int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x
   if (workspace_bytes < need) return RDFFT_ESPACE;
   if (outputs_overlap(args, 3)) return RDFFT_EOVERLAP;
   rdfft::CircMany c;
-  c.c_hat = c_hat, c.plan = plan;
+  c.in = x, c.g = g, c.c_hat = c_hat, c.out = grad_x, c.grad_c = grad_c, c.plan = plan;
   c.T = T, c.D = D, c.n = n;
-  cudaError_t e = cudaSuccess;
-  if (grad_c != nullptr) {
-    rdfft::GcSink sink;
-    sink.partial = need ? static_cast<float*>(workspace) : nullptr;
-    sink.partial_floats = (int64_t)(need / sizeof(float));
-    c.in = x, c.g = g, c.grad_c = grad_c;
-    e = rdfft::launch_circ_many(2, c, p, dtype, s, &sink);
-    if (e == cudaSuccess) e = rdfft::finish_grad_c(sink, grad_c, (int64_t)n * (D / p) * (D / p), p, s);
-  }
-  if (e == cudaSuccess && grad_x != nullptr) {
-    c.in = g, c.out = grad_x;
-    e = rdfft::launch_circ_many(1, c, p, dtype, s, nullptr);
-  }
-  return finish(e);
+  rdfft::GcSink sink;
+  sink.partial = static_cast<float*>(workspace);
+  sink.partial_floats = (int64_t)(need / sizeof(float));
+  return finish(rdfft::launch_circ_many_bwd(c, p, dtype, s, &sink));
 }
 
 int grad_norm_workspace_size(int count, size_t* bytes) {

@@ -358,18 +358,22 @@ int circ_fwd_many(const void* x, const float* c_hat, const void* base, void* y, 
                   int p, int n, int dtype, rdfft_stream_t stream);
 
 /*
- * circ_bwd_many_workspace_size -- device workspace, in bytes, of circ_bwd_many with grad_c for
- * these sizes on the current device (0: none needed). Needs no GPU, as circ_bwd_workspace_size.
+ * circ_bwd_many_workspace_size -- device workspace, in bytes, of circ_bwd_many for these sizes on
+ * the current device, with grad_c requested and grad_x too when with_grad_x != 0 (0 for T = 0):
+ * (token slices + n) x q x q x p x 4. Needs no GPU, as circ_bwd_workspace_size.
  */
-int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, size_t* bytes);
+int circ_bwd_many_workspace_size(int64_t T, int D, int p, int n, int dtype, int with_grad_x, size_t* bytes);
 
 /*
  * circ_bwd_many -- gradients of circ_fwd_many for upstream gradient g (the gradient of base is g):
  *     grad_x_t = W(c_k)^T g_t (zeros for a token without an adapter),
  *     grad_c[k] : as circ_bwd's grad_c, summed over the tokens of adapter k (zeros without any).
  *   grad_x : T x D of `dtype`, or NULL.   grad_c : n x q x q x p fp32, overwritten, or NULL.
- *   workspace : circ_bwd_many_workspace_size bytes, as circ_bwd_deterministic: the token slices
- *               are summed in a fixed order, so grad_c is the same on every run.
+ *   workspace : circ_bwd_many_workspace_size bytes (needed with grad_c, else it may be NULL),
+ *               as circ_bwd_deterministic: the token slices are summed in a fixed order, so
+ *               grad_c is the same on every run.
+ * What a skipped gradient alone needs may be NULL: x for grad_c, c_hat for grad_x. A timed-out
+ * wait (rdfft_take_device_error) leaves part of the outputs unwritten, as with circ_bwd.
  */
 int circ_bwd_many(const void* g, const void* x, const float* c_hat, void* grad_x, float* grad_c, const int32_t* plan,
                   int64_t T, int D, int p, int n, int dtype, void* workspace, size_t workspace_bytes,
