@@ -1,17 +1,23 @@
 // Grouping of a batch's tokens by adapter: a stable counting sort of T keys in [0, n], and
 // the tile lists that the adapter kernels' CTAs read (layout in adapter_plan.h).
 //
-// One CTA of 32 warps; warp w owns a contiguous range of tokens, so counting per warp and
-// then scanning the warps' counts of a bin gives every token a rank that keeps the batch's
-// order, with no atomics and the same result on every run. Lanes with equal keys find each
-// other with a match; the first of them moves the warp's counter. The keys are read twice
-// (4 T bytes, the second time from cache) and 8 T bytes and the lists are written.
+// One cluster of 1 to 8 CTAs of 32 warps; every warp owns a contiguous range of tokens, so
+// counting per warp and then scanning the warps' counts of a bin (over the cluster through
+// distributed shared memory) gives every token a rank that keeps the batch's order, with no
+// atomics and the same result on every run. Lanes with equal keys find each other with a match;
+// the first of them moves the warp's counter. The keys are read twice (4 T bytes, the second
+// time from cache) and 8 T bytes and the lists are written, but a few microseconds of latency,
+// not the bytes, are the time: a warp's steps of 32 tokens depend on one another (about 0.35 us
+// a step over both passes), so the CTAs are chosen for few steps per warp: T = 32768, 200
+// adapters: one CTA 24 us, eight 8.0 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "adapter_plan.h"
 #include "internal.h"
+#include "lora.cuh"
 #include "pdl.cuh"
+#include "rdfft.h"
 
 namespace rdfft {
 
@@ -20,20 +26,23 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
-__global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict__ ids, int T, int n, int* plan,
+__global__ void __launch_bounds__(kThreads, 1) k_adapter_plan(const int* __restrict__ ids, int T, int n, int* plan,
                                                            PlanLayout lay) {
   extern __shared__ int sm[];
   const int bins = n + 1;
   int* hist = sm;                             // [kWarps][bins]: counts, then next sorted position
   int* first = sm + kWarps * bins;            // [bins + 1]: offsets
   int* tile0 = first + bins + 1;              // [kPlanLists][bins + 1]: first tile of each group
+  int* mine_all = tile0 + kPlanLists * (bins + 1);   // [bins]: this CTA's counts
+  int* before = mine_all + bins;              // [bins]: tokens of the group in earlier CTAs
+  const unsigned C = cluster_size(), rank = cluster_rank();
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int i = threadIdx.x; i < kWarps * bins; i += kThreads) hist[i] = 0;
   griddep_wait();                             // ids are complete, readers of the old plan are done
   __syncthreads();
 
-  const int per = (T + kThreads - 1) / kThreads * 32;                 // tokens per warp, whole steps
-  const int64_t beg64 = (int64_t)w * per;
+  const int per = (T / (kThreads * (int)C) + 1) * 32;                 // tokens per warp, whole steps
+  const int64_t beg64 = ((int64_t)rank * kWarps + w) * per;
   const int beg = beg64 < T ? (int)beg64 : T, end = T - beg < per ? T : beg + per;
   int* mine = hist + w * bins;
   auto key_at = [&](int t) {                  // an id outside [0, n) is "no adapter": bin n
@@ -58,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict
   }
   __syncthreads();
 
-  // per bin: the warps' counts become ranks within the group
+  // per bin: the warps' counts become ranks within the CTA's part of the group
   for (int b = threadIdx.x; b < bins; b += kThreads) {
     int sum = 0;
 #pragma unroll 8
@@ -67,10 +76,29 @@ __global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict
       hist[i * bins + b] = sum;
       sum += c;
     }
+    mine_all[b] = sum;
+  }
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  for (int b = threadIdx.x; b < bins; b += kThreads) {
+    int sum = 0, ahead = 0, v[8];
+#pragma unroll
+    for (unsigned c = 0; c < 8; ++c) v[c] = c < C ? ld_cluster_i1(map_rank(mine_all + b, c)) : 0;
+#pragma unroll
+    for (unsigned c = 0; c < 8; ++c) {
+      if (c < rank) ahead += v[c];
+      sum += v[c];
+    }
+    before[b] = ahead;
     first[b] = sum;
 #pragma unroll
     for (int l = 0; l < kPlanLists; ++l) tile0[l * (bins + 1) + b] = (sum + plan_tile(l) - 1) / plan_tile(l);
   }
+  if (C > 1) cluster_arrive();                // done with the others' counts
   __syncthreads();
   // exclusive scans of the counts (warp 0) and of each list's tiles (warps 1 to 3)
   if (w <= kPlanLists) {
@@ -90,15 +118,16 @@ __global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict
     }
     if (lane == 0) {
       v[bins] = carry;
-      if (w > 0) plan[1 + w] = carry;
+      if (w > 0 && rank == 0) plan[1 + w] = carry;
     }
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && rank == 0) {
     plan[0] = T;
     plan[1] = n;
   }
   __syncthreads();
-  for (int b = threadIdx.x; b <= bins; b += kThreads) plan[lay.offsets + b] = first[b];
+  if (rank == 0)
+    for (int b = threadIdx.x; b <= bins; b += kThreads) plan[lay.offsets + b] = first[b];
 
   // the ranks place the tokens; the first token of every tile writes the tile
   for (int t0 = beg; t0 < end; t0 += 32 * kAhead) {
@@ -115,14 +144,14 @@ __global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict
       if (t < end) base = mine[key[s]];
       __syncwarp();
       if (t < end) {
-        const int rank = base + __popc(same & ((1u << lane) - 1));
-        const int pos = first[key[s]] + rank;
+        const int at = before[key[s]] + base + __popc(same & ((1u << lane) - 1));
+        const int pos = first[key[s]] + at;
         plan[lay.order + pos] = t;
         plan[lay.group + pos] = key[s];
 #pragma unroll
         for (int l = 0; l < kPlanLists; ++l)
-          if (rank % plan_tile(l) == 0) {
-            const int64_t tile = tile0[l * (bins + 1) + key[s]] + rank / plan_tile(l);
+          if (at % plan_tile(l) == 0) {
+            const int64_t tile = tile0[l * (bins + 1) + key[s]] + at / plan_tile(l);
             *reinterpret_cast<int2*>(plan + lay.tiles[l] + 2 * tile) = make_int2(pos, key[s]);
           }
         if (lane == __ffs(same) - 1) mine[key[s]] = base + __popc(same);
@@ -130,19 +159,22 @@ __global__ void __launch_bounds__(kThreads) k_adapter_plan(const int* __restrict
       __syncwarp();
     }
   }
+  if (C > 1) cluster_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_adapter_plan(const int* ids, int64_t T, int n, int* plan, cudaStream_t s) {
   const int bins = n + 1;
-  const size_t smem = sizeof(int) * ((size_t)kWarps * bins + (size_t)(kPlanLists + 1) * (bins + 1));
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_adapter_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(k_adapter_plan, dim3(1), dim3(kThreads), smem, s, ids, (int)T, n, plan, plan_layout(T, n));
+  const size_t smem = sizeof(int) * ((size_t)(kWarps + 2) * bins + (size_t)(kPlanLists + 1) * (bins + 1));
+  // the most that any n needs
+  const cudaError_t e = allow_smem<k_adapter_plan>(sizeof(int) * (size_t)(kWarps + 6) * (RDFFT_MAX_ADAPTERS + 2));
+  if (e != cudaSuccess) return e;
+  // about two steps per warp (2048 tokens per CTA)
+  int cluster = 1;
+  while (cluster < 8 && (int64_t)cluster * 2048 < T) cluster *= 2;
+  return launch_cluster_pdl(k_adapter_plan, dim3(cluster), dim3(kThreads), cluster, smem, s, ids, (int)T, n, plan,
+                            plan_layout(T, n));
 }
 
 }  // namespace rdfft

@@ -9,7 +9,9 @@
 
 #include <vector>
 
+#include "adapter_plan.h"
 #include "layer_policy.h"
+#include "many_policy.h"
 #include "rdfft2d_steps.cuh"
 #include "rdfft_steps.cuh"
 
@@ -320,6 +322,22 @@ int rdfft_layer_gc_half_tiles(int64_t B, int tt, int q, int hb, int64_t max_slot
 }
 int rdfft_layer_gc_slices(int njgroups, int64_t ntiles, int n_sm, int64_t* tiles_per) {
   return rdfft::layer_gc_slices(njgroups, ntiles, n_sm, tiles_per);
+}
+
+// The many-adapter rules (many_policy.h, adapter_plan.h), for the CPU tests.
+int64_t rdfft_plan_tile_cap(int64_t T, int n, int tile) { return rdfft::plan_tile_cap(T, n, tile); }
+int rdfft_lora_list(int64_t T, int n) { return rdfft::lora_list(T, n); }
+int rdfft_lora_cluster(int64_t tiles, int list, int f32, int K, int N) {
+  return rdfft::lora_cluster(tiles, list, f32 != 0, K, N);
+}
+int rdfft_lora_token_split(int64_t T, int blocks, int chunk, int per_sm) {
+  return rdfft::lora_token_split(T, blocks, chunk, per_sm);
+}
+int rdfft_circ_many_tokens(int64_t T, int n, int q, int qi_max, int n_sm, int tt_max) {
+  return rdfft::circ_many_tokens(T, n, q, qi_max, n_sm, tt_max);
+}
+int rdfft_circ_many_slices(int64_t T, int n, int njgroups, int tt, int n_sm) {
+  return rdfft::circ_many_slices(T, n, njgroups, tt, n_sm);
 }
 
 // Positions of the first n elements of the generic orbit with residue r of a pass

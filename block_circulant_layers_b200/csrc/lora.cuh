@@ -154,6 +154,12 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ int ld_cluster_i1(uint32_t a) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // Sum over the cluster's CTAs of the four floats at `p`, in rank order; the loads go out together.
 __device__ __forceinline__ float4 cluster_sum_f4(const float* p, unsigned C) {
   float4 v[8];

@@ -315,33 +315,36 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&v)[4], uint32_t addr) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
+// Four 8 x 8 matrices to shared memory, held as ldsm4 loads them.
+__device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 // Byte offset of 16-byte unit `unit` of row `row` in a tile of W bf16 columns. The units of a
 // row are permuted by the row so that 8 rows' units of one column fall into different banks.
+// Moving by 16 rows adds 32 W; moving by an even number u of units from an even unit, or from
+// the odd one after it, flips 16 u in the offset.
 template <int W>
 __device__ __forceinline__ uint32_t at(int row, int unit) {
   const int f = W == 16 ? (row >> 2) & 1 : (W == 32 ? (row >> 1) & 3 : row & 7);
   return row * 2 * W + 16 * (unit ^ f);
 }
 
-// Fragments from a tile of W columns at `base`. Operand rows (tokens, or output columns) by
-// contraction index, 16 of each at (row0, k0), lie in the tile as they are (n: not transposed)
-// or with the contraction index as the row (t). An A fragment is one of them; for B, x4 gives
-// {b0, b1} of rows row0..+7 and of row0 + 8..+15.
+// Fragments from a tile of W columns: 16 rows from row0, 16 columns from col0 (multiples of 16).
+// A lane's address is an offset worked out once (lane_rows or lane_cols) moved to (row0, col0).
+// As ldsm4 gives them, lane_rows yields an A fragment whose rows are the tile's rows or, loaded
+// transposed, {b0, b1} of B columns col0..+7 and col0 + 8..+15 with the contraction index down the
+// rows; lane_cols yields {b0, b1} of B columns row0..+7 and row0 + 8..+15 that are the tile's rows
+// or, loaded transposed, an A fragment with the contraction index down the rows.
 template <int W>
-__device__ __forceinline__ void frag_a_n(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
-  ldsm4(v, base + at<W>(row0 + (lane / 8 & 1) * 8 + lane % 8, k0 / 8 + lane / 16));
-}
+__device__ __forceinline__ uint32_t lane_rows(int lane) { return at<W>((lane / 8 & 1) * 8 + lane % 8, lane / 16); }
 template <int W>
-__device__ __forceinline__ void frag_a_t(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
-  ldsm4t(v, base + at<W>(k0 + lane / 16 * 8 + lane % 8, row0 / 8 + (lane / 8 & 1)));
-}
+__device__ __forceinline__ uint32_t lane_cols(int lane) { return at<W>(lane / 16 * 8 + lane % 8, lane / 8 & 1); }
 template <int W>
-__device__ __forceinline__ void frag_b_n(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
-  ldsm4(v, base + at<W>(row0 + lane / 16 * 8 + lane % 8, k0 / 8 + (lane / 8 & 1)));
-}
-template <int W>
-__device__ __forceinline__ void frag_b_t(uint32_t (&v)[4], uint32_t base, int row0, int k0, int lane) {
-  ldsm4t(v, base + at<W>(k0 + (lane / 8 & 1) * 8 + lane % 8, row0 / 8 + lane / 16));
+__device__ __forceinline__ uint32_t moved(uint32_t offset, int row0, int col0) {
+  return (offset ^ (2 * col0)) + row0 * 2 * W;
 }
 
 // ----------------------------------------------------------------- rows, 64-token tiles
@@ -429,6 +432,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   for (int s = 0; s < S::kStages - 1; ++s) request(s);
 
   const int wm = warp % 4, wh = warp / 4;                      // 16 rows; half of a step's columns
+  // fragment offsets: rows of in or base; w1; mid; w2
+  const uint32_t x_off = moved<COLS>(lane_rows<COLS>(lane), 16 * wm, 0);
+  const uint32_t w1_off = BWD ? lane_rows<R>(lane) : lane_cols<COLS>(lane);
+  const uint32_t mid_off = moved<R>(lane_rows<R>(lane), 16 * wm, 0);
+  const uint32_t w2_off = BWD ? lane_rows<COLS>(lane) : lane_cols<R>(lane);
   if (adapted) {
     float acc[R / 8][4];
 #pragma unroll
@@ -443,12 +451,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 #pragma unroll
       for (int k = COLS / 2 * wh; k < COLS / 2 * (wh + 1); k += 16) {
         uint32_t x[4];
-        frag_a_n<COLS>(x, x_at, 16 * wm, k, lane);
+        ldsm4(x, x_at + moved<COLS>(x_off, 0, k));
 #pragma unroll
         for (int j = 0; j < R / 16; ++j) {
           uint32_t w[4];
-          if constexpr (!BWD) frag_b_n<COLS>(w, w_at, 16 * j, k, lane);
-          else frag_b_t<R>(w, w_at, 16 * j, k, lane);
+          if constexpr (!BWD) ldsm4(w, w_at + moved<COLS>(w1_off, 16 * j, k));
+          else ldsm4t(w, w_at + moved<R>(w1_off, k, 16 * j));
           mma16816(acc[2 * j], x[0], x[1], x[2], x[3], w[0], w[1]);
           mma16816(acc[2 * j + 1], x[0], x[1], x[2], x[3], w[2], w[3]);
         }
@@ -507,35 +515,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
     unsigned char* const tile_p = ring + step % S::kStages * S::kStage;
     const uint32_t w_at = ring_at + step % S::kStages * S::kStage + S::kRowBytes;
     if (adapted) {
+      // the sums start from base, whose fragments lie in the stage as the results will
+      const uint32_t out_at = ring_at + step % S::kStages * S::kStage;
       float acc[COLS / 16][4];
 #pragma unroll
-      for (int j = 0; j < COLS / 16; ++j)
+      for (int j = 0; j < COLS / 32; ++j) {
+        uint32_t b[4] = {0, 0, 0, 0};
+        if (a.base != nullptr) ldsm4(b, out_at + moved<COLS>(x_off, 0, COLS / 2 * wh + 16 * j));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) {                          // rows g + 8 (e & 1), columns 8 (e / 2) + 2 q
+          acc[2 * j + e / 2][2 * (e & 1)] = lo_f32(b[e]);
+          acc[2 * j + e / 2][2 * (e & 1) + 1] = hi_f32(b[e]);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < R; k += 16) {
         uint32_t h[4], l[4];
-        frag_a_n<R>(h, hi_at, 16 * wm, k, lane);
-        frag_a_n<R>(l, lo_at, 16 * wm, k, lane);
+        ldsm4(h, hi_at + moved<R>(mid_off, 0, k));
+        ldsm4(l, lo_at + moved<R>(mid_off, 0, k));
 #pragma unroll
         for (int j = 0; j < COLS / 32; ++j) {
           uint32_t w[4];
-          if constexpr (!BWD) frag_b_n<R>(w, w_at, COLS / 2 * wh + 16 * j, k, lane);
-          else frag_b_t<COLS>(w, w_at, COLS / 2 * wh + 16 * j, k, lane);
+          if constexpr (!BWD) ldsm4(w, w_at + moved<R>(w2_off, COLS / 2 * wh + 16 * j, k));
+          else ldsm4t(w, w_at + moved<COLS>(w2_off, k, COLS / 2 * wh + 16 * j));
           mma16816(acc[2 * j], h[0], h[1], h[2], h[3], w[0], w[1]);
           mma16816(acc[2 * j + 1], h[0], h[1], h[2], h[3], w[2], w[3]);
           mma16816(acc[2 * j], l[0], l[1], l[2], l[3], w[0], w[1]);
           mma16816(acc[2 * j + 1], l[0], l[1], l[2], l[3], w[2], w[3]);
         }
       }
-      // the sum with base replaces it in the stage (zeros where there is none)
 #pragma unroll
-      for (int j = 0; j < COLS / 16; ++j)
+      for (int j = 0; j < COLS / 32; ++j) {
+        uint32_t o[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(tile_p + at<COLS>(16 * wm + g + 8 * h, UNITS / 2 * wh + j) + 4 * q);
-          *p = pack2(acc[j][2 * h] + lo_f32(*p), acc[j][2 * h + 1] + hi_f32(*p));
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack2(acc[2 * j + e / 2][2 * (e & 1)], acc[2 * j + e / 2][2 * (e & 1) + 1]);
+        stsm4(out_at + moved<COLS>(x_off, 0, COLS / 2 * wh + 16 * j), o);
+      }
       __syncthreads();
     }
     const int c = COLS * (n_first + step - n1) + 8 * tunit;
@@ -596,6 +612,8 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   const float* const mid = is_a ? a.v : a.u;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
   const int wc = warp % S::kWC, rho0 = 16 * NI * (warp / S::kWC);
+  const uint32_t x_off = moved<COLS>(lane_rows<COLS>(lane), 0, 16 * wc);
+  const uint32_t m_off = moved<R>(lane_cols<R>(lane), 0, rho0);
   const TileShare share(a.plan, rank, C);
 
   float acc[NA];
@@ -699,7 +717,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
       for (int k = 0; k < S::kTok; k += 16) {
         if (k >= tokens) break;
         uint32_t b[4];
-        frag_b_t<COLS>(b, x_at, 16 * wc, k, lane);
+        ldsm4t(b, x_at + moved<COLS>(x_off, k, 0));
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           float(&d0)[4] = *reinterpret_cast<float(*)[4]>(acc + 8 * j);
@@ -707,7 +725,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             uint32_t f[4];
-            frag_a_t<R>(f, mid_at + s * S::kTok * R * 2, rho0 + 16 * j, k, lane);
+            ldsm4t(f, mid_at + s * S::kTok * R * 2 + moved<R>(m_off, k, 16 * j));
             mma16816(d0, f[0], f[1], f[2], f[3], b[0], b[1]);
             mma16816(d1, f[0], f[1], f[2], f[3], b[2], b[3]);
           }

@@ -14,6 +14,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
 
@@ -39,6 +40,7 @@ class _LowRankFn(torch.autograd.Function):
         return y.reshape(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x2, a2, b2, u, scale, _ = ctx.saved_tensors         # fails if the plan was made again
         need = ctx.needs_input_grad
@@ -63,6 +65,7 @@ class _CirculantManyFn(torch.autograd.Function):
         return y.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x2, c_hat, _ = ctx.saved_tensors                      # fails if the plan was made again
         need = ctx.needs_input_grad
@@ -79,6 +82,8 @@ def low_rank_many(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: _b.Ad
                   scale: torch.Tensor | None = None, base: torch.Tensor | None = None) -> torch.Tensor:
     """y_t = base_t + scale_k b_k (a_k x_t); a (n, r, K) and b (n, N, r) are used in x's dtype.
     scale (n,) float32 takes no gradient."""
+    if scale is not None and scale.requires_grad:
+        raise ValueError("scale takes no gradient")
     return _LowRankFn.apply(x, a, b, plan, scale, base)
 
 
