@@ -330,8 +330,8 @@ int rdfft_lora_list(int64_t T, int n) { return rdfft::lora_list(T, n); }
 int rdfft_lora_cluster(int64_t tiles, int list, int f32, int K, int N) {
   return rdfft::lora_cluster(tiles, list, f32 != 0, K, N);
 }
-int rdfft_lora_token_split(int64_t T, int blocks, int chunk, int per_sm) {
-  return rdfft::lora_token_split(T, blocks, chunk, per_sm);
+int rdfft_lora_token_split(int64_t T, int n, int blocks, int chunk, int per_sm) {
+  return rdfft::lora_token_split(T, n, blocks, chunk, per_sm);
 }
 int rdfft_circ_many_tokens(int64_t T, int n, int q, int qi_max, int n_sm, int tt_max) {
   return rdfft::circ_many_tokens(T, n, q, qi_max, n_sm, tt_max);

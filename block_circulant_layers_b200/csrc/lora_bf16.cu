@@ -656,9 +656,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
       if (i < count && tid < S::kTok) {
         const int pos = desc[i + 1].x + tid;
         const bool in = pos < desc[i + 2].x;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(shared_at(&order[i % S::kOrders][tid])),
-                     "l"(in ? a.plan.order + pos : a.plan.order), "r"(in ? 4 : 0)
-                     : "memory");
+        cp4(shared_at(&order[i % S::kOrders][tid]), in ? a.plan.order + pos : a.plan.order, in);
       }
     };
     auto request = [&](int i) {
@@ -795,7 +793,7 @@ cudaError_t run_wgrad(const LoraWgrad<bf16_t>& a, cudaStream_t s) {
   const int ka = (a.K + S::kCols - 1) / S::kCols, nb = (a.N + S::kCols - 1) / S::kCols;
   const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
   // by both widths, so that a gradient does not depend on whether the other is asked for
-  const int cluster = lora_token_split(a.plan.T, ka + nb, S::kTok, S::kPerSM);
+  const int cluster = lora_token_split(a.plan.T, a.plan.n, ka + nb, S::kTok, S::kPerSM);
   return launch_cluster_pdl(k_lora_wgrad<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, S::smem, s,
                             a, ba);
 }

@@ -1,8 +1,8 @@
 // Low-rank adapters of many requests, fp32: rows kernel (forward, grad_x) and weight
 // gradients. The same split as lora_bf16.cu (one cluster per tile of the plan, one launch),
 // with the products as fp32 FMAs on register tiles fed from shared memory: the parity bar of
-// fp32 leaves no room for tf32 operands. Steps of 32 contraction indices, then of 64 output
-// columns, pass through one ring of cp.async stages; operands keep their own row order, padded
+// fp32 leaves no room for tf32 operands. Steps of 32 or 64 contraction indices, then of 64
+// output columns, pass through one ring of cp.async stages; operands keep their own row order, padded
 // by 16 bytes a row, and are read 4 contraction indices at a time.
 #include "lora.cuh"
 
@@ -13,7 +13,6 @@ namespace rdfft {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKC = 32;                        // contraction indices per step
 constexpr int kNC = 64;                        // output columns per step
 
 // N consecutive floats of shared memory.
@@ -37,6 +36,7 @@ __device__ __forceinline__ float4 ldg4(const float* p) { return __ldg(reinterpre
 
 template <int R, int M, bool BWD>
 struct RowsShape {
+  static constexpr int kKC = M == 16 && R <= 64 ? 64 : 32;  // contraction indices per step
   static constexpr int KG = 64 / M;                         // thread groups that share a step's indices
   static constexpr int XS = kKC + 4;                        // padded strides: in,
   static constexpr int W1S = BWD ? R + 4 : kKC + 4;         // w1 (backward: contraction index outermost),
@@ -52,7 +52,7 @@ struct RowsShape {
 template <int R, int M, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   using S = RowsShape<R, M, BWD>;
-  constexpr int RT = R / 16;                                // r values per thread
+  constexpr int RT = R / 16, kKC = S::kKC, KU = kKC / 4;    // r values per thread; 16-byte units per row of a step
   extern __shared__ __align__(16) float sm[];               // ring
   float* const part = sm + S::kStage * S::kStages;          // [KG][M][R]
   float* const mid = part + S::kPart;                       // [M][MS]
@@ -68,18 +68,18 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   const int tid = threadIdx.x, K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
 
-  // this CTA's steps: [0, n1) of 32 columns of in and w1, then [n1, n1 + n2) of 64 of w2
+  // this CTA's steps: [0, n1) of kKC columns of in and w1, then [n1, n1 + n2) of 64 of w2
   const int ks = (K + kKC - 1) / kKC, ns = (N + kNC - 1) / kNC;
   const int k_first = (int)((int64_t)ks * rank / C), n_first = (int)((int64_t)ns * rank / C);
   const int n1 = adapted ? (int)((int64_t)ks * (rank + 1) / C) - k_first : 0;
   const int n2 = (a.out != nullptr && (adapted || a.base != a.out)) ? (int)((int64_t)ns * (rank + 1) / C) - n_first : 0;
   const float* const w1 = a.w1 + (adapted ? (int64_t)ad * r * K : 0);
   const float* const w2 = a.w2 + (adapted ? (int64_t)ad * r * N : 0);
-  constexpr int XL = (M * 8 + kThreads - 1) / kThreads;
+  constexpr int XL = (M * KU + kThreads - 1) / kThreads;
   int xtok[XL];
 #pragma unroll
   for (int i = 0; i < XL; ++i) {
-    const int t = (tid + kThreads * i) / 8;
+    const int t = (tid + kThreads * i) / KU;
     xtok[i] = t < m ? __ldg(a.plan.order + pos0 + t) : -1;
   }
   auto request = [&](int step) {
@@ -89,19 +89,19 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
         const int k0 = kKC * (k_first + step);
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
-          const int e = tid + kThreads * i, k = k0 + e % 8 * 4;
+          const int e = tid + kThreads * i, k = k0 + e % KU * 4;
           const bool in = xtok[i] >= 0 && k < K;
-          if (e < M * 8) cp16(dst + (e / 8 * S::XS + e % 8 * 4) * 4, in ? a.in + (int64_t)xtok[i] * K + k : a.in, in);
+          if (e < M * KU) cp16(dst + (e / KU * S::XS + e % KU * 4) * 4, in ? a.in + (int64_t)xtok[i] * K + k : a.in, in);
         }
         const uint32_t wdst = dst + M * S::XS * 4;
 #pragma unroll
-        for (int i = 0; i < (R * 8 + kThreads - 1) / kThreads; ++i) {
+        for (int i = 0; i < (R * KU + kThreads - 1) / kThreads; ++i) {
           const int e = tid + kThreads * i;
-          if (R * 8 < kThreads && e >= R * 8) break;
+          if (R * KU < kThreads && e >= R * KU) break;
           if constexpr (!BWD) {
-            const int rho = e / 8, k = k0 + e % 8 * 4;
+            const int rho = e / KU, k = k0 + e % KU * 4;
             const bool in = rho < r && k < K;
-            cp16(wdst + (rho * S::W1S + e % 8 * 4) * 4, in ? w1 + (int64_t)rho * K + k : w1, in);
+            cp16(wdst + (rho * S::W1S + e % KU * 4) * 4, in ? w1 + (int64_t)rho * K + k : w1, in);
           } else {
             const int k = k0 + e / (R / 4), rho = e % (R / 4) * 4;
             const bool in = rho < r && k < K;
@@ -282,22 +282,33 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 
 // ------------------------------------------------------------------- weight gradients
 // One cluster: 64 columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
-// plan's 64-token tiles evenly (TileShare); 4 columns x R / 16 values of r per thread. An
-// adapter whose tiles lie in several CTAs is written by the first of them, as in lora_bf16.cu.
-constexpr int kTok = 64;
+// plan's 64-token tiles evenly (TileShare), as in lora_bf16.cu: tiles through a ring of two
+// cp.async stages, an adapter whose tiles lie in several CTAs written by the first of them. A
+// thread has 4 columns x RT values of r, of a share of the tile's tokens while r <= 32 (a
+// smaller register tile would read shared memory as often as it multiplies); the shares are
+// added in order when an adapter is complete.
 template <int R>
-constexpr int wgrad_per_sm() { return R <= 32 ? 3 : (R == 64 ? 2 : 1); }
-template <int R>
-constexpr size_t wgrad_smem() { return sizeof(float) * (kTok * (64 + 4) + kTok * (R + 4) + R * 64); }
+struct WgradF32 {
+  static constexpr int kTok = 64, kStages = 2, kOrders = 8;
+  static constexpr int RT = R <= 64 ? 4 : 8;                // values of r per thread
+  static constexpr int TG = kThreads / (16 * (R / RT));     // token shares
+  static constexpr int XS = 64 + 4, WS = R + 4;
+  static constexpr int kStage = kTok * (XS + WS);
+  static constexpr int SS = 64 + 1;                         // padded row of a share's sums
+  static constexpr int kShare = R * SS;
+  static constexpr int kPerSM = R == 16 ? 3 : (R <= 64 ? 2 : 1);          // CTAs that fit
+  static constexpr size_t smem = sizeof(float) * (size_t)(kStage * kStages + R * 64 + (TG > 1 ? TG * kShare : 0));
+};
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, wgrad_per_sm<R>()) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
-  constexpr int RT = R / 16, XS = 64 + 4, WS = R + 4;
-  extern __shared__ __align__(16) float sm[];
-  float* const xs = sm;                                     // [kTok][XS]
-  float* const ws = sm + kTok * XS;                         // [kTok][WS]
-  float* const head = ws + kTok * WS;                       // [4 RT][kThreads]
+__global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
+  using S = WgradF32<R>;
+  constexpr int RT = S::RT, TG = S::TG, NA = R * 64 / kThreads;
+  extern __shared__ __align__(16) float sm[];               // ring
+  float* const head = sm + S::kStage * S::kStages;          // [NA][kThreads]
+  float* const shares = head + R * 64;                      // [TG][R][SS]
   __shared__ int2 desc[kWindow + 2];
+  __shared__ __align__(16) int order[S::kOrders][S::kTok];
   griddep_wait();
   if (!plan_matches(a.plan)) return;
   const unsigned C = cluster_size(), rank = cluster_rank();
@@ -307,8 +318,7 @@ __global__ void __launch_bounds__(kThreads, wgrad_per_sm<R>()) k_lora_wgrad_f32(
   const int W = is_a ? a.K : a.N;
   const float* const rows = is_a ? a.x : a.g;
   const float* const mid = is_a ? a.v : a.u;
-  // consecutive threads write consecutive elements: columns for grad_a, r for grad_b
-  const int cg = is_a ? tid % 16 : tid / 16, rg = is_a ? tid / 16 : tid % 16;
+  const int tg = tid / (kThreads / TG), cg = tid % 16, rg = tid % (kThreads / TG) / 16;
   const TileShare share(a.plan, rank, C);
   float acc[4][RT];
   auto clear = [&] {
@@ -317,86 +327,148 @@ __global__ void __launch_bounds__(kThreads, wgrad_per_sm<R>()) k_lora_wgrad_f32(
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
   };
+  // The complete sums, four consecutive elements of the gradient (columns for grad_a, r for
+  // grad_b) at a time: sum[4 v..] belongs at (rho, c) and after. One share: the register tile as
+  // it is. Several: values of all of them, added in order through shared memory.
+  float sum[NA];
+  auto index = [&](int v, int& rho, int& c) {
+    if constexpr (TG == 1) {
+      rho = RT * rg + (is_a ? v : v % (RT / 4) * 4);
+      c = 4 * cg + (is_a ? 0 : v / (RT / 4));
+    } else {
+      const int k = tid + kThreads * v;
+      rho = is_a ? k / 16 : k % (R / 4) * 4;
+      c = is_a ? k % 16 * 4 : k / (R / 4);
+    }
+  };
+  auto collect = [&] {
+    if constexpr (TG == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const float v = acc[i][j];
+          if (is_a) sum[4 * j + i] = v;
+          else sum[RT * i + j] = v;
+        }
+    } else {
+      float* const to = shares + tg * S::kShare;
+      __syncthreads();                                      // the last sums have been read
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[(RT * rg + j) * S::SS + 4 * cg + i] = acc[i][j];
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < NA / 4; ++v) {
+        int rho, c;
+        index(v, rho, c);
+        const float* from = shares + rho * S::SS + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int o = e * (is_a ? 1 : S::SS);
+          float t = from[o];
+#pragma unroll
+          for (int k = 1; k < TG; ++k) t += from[k * S::kShare + o];
+          sum[4 * v + e] = t;
+        }
+      }
+    }
+  };
   auto write = [&](int ad) {
     const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rho = RT * rg + j, c = n0 + 4 * cg + i;
-        if (rho >= r || c >= W) continue;
-        if (is_a)
-          a.grad_a[((int64_t)ad * r + rho) * W + c] = acc[i][j];
-        else
-          a.grad_b[((int64_t)ad * W + c) * r + rho] = scale * acc[i][j];
-      }
-  };
-  constexpr int XL = kTok * 16 / kThreads, WL = kTok * R / 4 / kThreads;
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float4 xv[XL], wv[WL];
-  auto fetch = [&](int p0, int tokens) {
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      const int e = tid + kThreads * i, k = e / 16, c = n0 + e % 16 * 4;
-      xv[i] = (k < tokens && c < W) ? ldg4(rows + (int64_t)__ldg(a.plan.order + p0 + k) * W + c) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < WL; ++i) {
-      const int e = tid + kThreads * i, k = e / (R / 4), rho = e % (R / 4) * 4;
-      wv[i] = (k < tokens && rho < r) ? ldg4(mid + (int64_t)__ldg(a.plan.order + p0 + k) * r + rho) : zero;
+    for (int v = 0; v < NA / 4; ++v) {
+      int rho, c;
+      index(v, rho, c);
+      if (rho >= r || n0 + c >= W) continue;                // r and W are multiples of 8: all four or none
+      float* const dst = is_a ? a.grad_a + ((int64_t)ad * r + rho) * W + n0 + c
+                              : a.grad_b + ((int64_t)ad * W + n0 + c) * r + rho;
+      *reinterpret_cast<float4*>(dst) = make_float4(scale * sum[4 * v], scale * sum[4 * v + 1], scale * sum[4 * v + 2],
+                                                    scale * sum[4 * v + 3]);
     }
   };
+
   clear();
   int open = -1;                                            // adapter whose sums go on in the next CTA
   bool from_before = false;                                 // the sum at hand began in an earlier CTA
   for (int w0 = share.lo; w0 < share.hi; w0 += kWindow) {
     const int count = min(kWindow, share.hi - w0);
-    __syncthreads();
+    __syncthreads();                                        // the last window is consumed
     share.window(a.plan, w0, desc);
     __syncthreads();
+    auto request_order = [&](int i) {
+      if (i < count && tid < S::kTok) {
+        const int pos = desc[i + 1].x + tid;
+        const bool in = pos < desc[i + 2].x;
+        cp4(shared_at(&order[i % S::kOrders][tid]), in ? a.plan.order + pos : a.plan.order, in);
+      }
+    };
+    auto request = [&](int i) {
+      if (i < count) {
+        const int tokens = desc[i + 2].x - desc[i + 1].x;
+        const int* const ord = order[i % S::kOrders];
+        const uint32_t xs = shared_at(sm + i % S::kStages * S::kStage), ws = xs + S::kTok * S::XS * 4;
+#pragma unroll
+        for (int h = 0; h < S::kTok * 16 / kThreads; ++h) {
+          const int e = tid + kThreads * h, t = e / 16, c = n0 + e % 16 * 4;
+          const bool in = t < tokens && c < W;
+          cp16(xs + (t * S::XS + e % 16 * 4) * 4, in ? rows + (int64_t)ord[t] * W + c : rows, in);
+        }
+#pragma unroll
+        for (int h = 0; h < S::kTok * R / 4 / kThreads; ++h) {
+          const int e = tid + kThreads * h, t = e / (R / 4), c = e % (R / 4) * 4;
+          const bool in = t < tokens && c < r;
+          cp16(ws + (t * S::WS + c) * 4, in ? mid + (int64_t)ord[t] * r + c : mid, in);
+        }
+      }
+    };
+    request_order(0);
+    request_order(1);
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    request(0);
+    request_order(2);
+    cp_commit();
     if (w0 == share.lo) from_before = desc[0].y == desc[1].y;
-    fetch(desc[1].x, desc[2].x - desc[1].x);
     for (int i = 0; i < count; ++i) {
-      __syncthreads();                                      // the last tile is consumed
-#pragma unroll
-      for (int h = 0; h < XL; ++h) {
-        const int e = tid + kThreads * h;
-        *reinterpret_cast<float4*>(xs + e / 16 * XS + e % 16 * 4) = xv[h];
-      }
-#pragma unroll
-      for (int h = 0; h < WL; ++h) {
-        const int e = tid + kThreads * h;
-        *reinterpret_cast<float4*>(ws + e / (R / 4) * WS + e % (R / 4) * 4) = wv[h];
-      }
+      cp_wait<0>();                                         // rows i and order i + 1 have arrived
       __syncthreads();
+      const bool goes_on = desc[i + 2].y == desc[i + 1].y;  // the next tile is the same adapter's
+      const bool ends = !goes_on || w0 + i + 1 == share.hi;
+      request(i + 1);
+      request_order(i + 3);
+      cp_commit();
       const int tokens = desc[i + 2].x - desc[i + 1].x, ad = desc[i + 1].y;
-      if (i + 1 < count) fetch(desc[i + 2].x, desc[i + 3].x - desc[i + 2].x);
-#pragma unroll 8
-      for (int k = 0; k < tokens; ++k) {
+      const float* const xs = sm + i % S::kStages * S::kStage;
+      const float* const ws = xs + S::kTok * S::XS;
+      const int t1 = min(tokens, (tg + 1) * (S::kTok / TG));
+#pragma unroll 4
+      for (int k = tg * (S::kTok / TG); k < t1; ++k) {
         float xr[4], wr[RT];
-        lds<4>(xs + k * XS + 4 * cg, xr);
-        lds<RT>(ws + k * WS + RT * rg, wr);
+        lds<4>(xs + k * S::XS + 4 * cg, xr);
+        lds<RT>(ws + k * S::WS + RT * rg, wr);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int j = 0; j < RT; ++j) acc[x][j] = fmaf(xr[x], wr[j], acc[x][j]);
       }
-      const bool goes_on = desc[i + 2].y == ad;             // the next tile is the same adapter's
-      if (w0 + i + 1 == share.hi && goes_on && !from_before) {
-        open = ad;                                          // its sums stay here
-      } else if (!goes_on || w0 + i + 1 == share.hi) {
-        if (from_before) {                                  // an earlier CTA writes it
+      if (ends) {
+        collect();
+        clear();
+        if (goes_on && !from_before) {
+          open = ad;                                        // its sums stay here
+        } else if (from_before) {                           // an earlier CTA writes it
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int j = 0; j < RT; ++j) head[(x * RT + j) * kThreads + tid] = acc[x][j];
+          for (int e = 0; e < NA; ++e) head[e * kThreads + tid] = sum[e];
           from_before = false;
         } else {
           write(ad);
         }
-        clear();
       }
     }
+    cp_wait<0>();
   }
   griddep_launch_dependents();
   if (C > 1) {
@@ -408,13 +480,14 @@ __global__ void __launch_bounds__(kThreads, wgrad_per_sm<R>()) k_lora_wgrad_f32(
         const int klo = (int)((int64_t)share.all * k / C), khi = (int)((int64_t)share.all * (k + 1) / C);
         if (klo == khi) continue;                           // no tiles there
         if (__ldg(a.plan.tiles + klo).y != open) break;
-        add_from(*reinterpret_cast<float(*)[4 * RT]>(acc), head, k);
+        add_from(sum, head, k);
       }
       write(open);
     }
     cluster_arrive();
   }
-  clear();
+#pragma unroll
+  for (int e = 0; e < NA; ++e) sum[e] = 0.0f;
   for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens
     if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
   if (C > 1) cluster_wait();                                // the others are done with this CTA's memory
@@ -449,15 +522,15 @@ cudaError_t rows_r(const LoraRows<float>& a, const int* plan, int64_t T, int n, 
 
 template <int R>
 cudaError_t run_wgrad(const LoraWgrad<float>& a, cudaStream_t s) {
+  using S = WgradF32<R>;
+  const cudaError_t e = allow_smem<k_lora_wgrad_f32<R>>(S::smem);
+  if (e != cudaSuccess) return e;
   const int ka = (a.K + 63) / 64, nb = (a.N + 63) / 64;
   const int ba = a.grad_a ? ka : 0, bb = a.grad_b ? nb : 0;
-  constexpr size_t smem = wgrad_smem<R>();
-  const cudaError_t e = allow_smem<k_lora_wgrad_f32<R>>(smem);
-  if (e != cudaSuccess) return e;
   // by both widths, so that a gradient does not depend on whether the other is asked for
-  const int cluster = lora_token_split(a.plan.T, ka + nb, kTok, wgrad_per_sm<R>());
-  return launch_cluster_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, smem, s,
-                            a, ba);
+  const int cluster = lora_token_split(a.plan.T, a.plan.n, ka + nb, S::kTok, S::kPerSM);
+  return launch_cluster_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster,
+                            S::smem, s, a, ba);
 }
 
 }  // namespace

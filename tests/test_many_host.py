@@ -23,7 +23,7 @@ def emu():
     L.rdfft_plan_tile_cap.argtypes, L.rdfft_plan_tile_cap.restype = [i64, i32, i32], i64
     L.rdfft_lora_list.argtypes = [i64, i32]
     L.rdfft_lora_cluster.argtypes = [i64, i32, i32, i32, i32]
-    L.rdfft_lora_token_split.argtypes = [i64, i32, i32, i32]
+    L.rdfft_lora_token_split.argtypes = [i64, i32, i32, i32, i32]
     L.rdfft_circ_many_tokens.argtypes = [i64, i32, i32, i32, i32, i32]
     L.rdfft_circ_many_slices.argtypes = [i64, i32, i32, i32, i32]
     return L
@@ -73,7 +73,7 @@ def test_rules_stay_in_their_ranges(emu):
             c = emu.rdfft_lora_cluster(tiles, lst, is_f32, K, N)
             assert c in (1, 2, 4, 8) and tiles * c < 2 ** 31
         for per_sm in (1, 2, 3):
-            c = emu.rdfft_lora_token_split(T, (K + 63) // 64 + (N + 63) // 64, 64, per_sm)
+            c = emu.rdfft_lora_token_split(T, n, (K + 63) // 64 + (N + 63) // 64, 64, per_sm)
             assert 1 <= c <= 8
         q = rng.choice([1, 2, 3, 8, 32, 128])
         assert emu.rdfft_circ_many_tokens(T, n, q, 8, 148, 4) in (1, 2, 4)
