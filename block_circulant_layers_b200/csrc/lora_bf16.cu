@@ -566,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 }
 
 // ------------------------------------------------------------------- weight gradients
-// One cluster: 128 (64 at r > 64) columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
+// One cluster: 128 (64 at r > 32) columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
 // plan's 64-token tiles evenly (TileShare). D[rho, column] = sum_t mid[t, rho] row[t, column]:
 // tokens are the contraction index, and both operands are read transposed. A warp has 16
-// columns and every rho (half of them at r > 64), so no sums are shared inside a CTA. An adapter whose tiles lie in
+// columns and every rho (half of them at r > 32), so no sums are shared inside a CTA. An adapter whose tiles lie in
 // several CTAs is written by the first of them, which adds the others' sums in rank order
 // through distributed shared memory.
 // Tiles pass through a ring of cp.async stages: a tile's rows are requested one or two steps
@@ -578,9 +578,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 // (24 mantissa bits), since the gradients are fp32.
 template <int R>
 struct Wgrad {
-  static constexpr int kCols = R <= 64 ? 128 : 64, kTok = 64, kOrders = 8;
-  static constexpr int kStages = R <= 32 ? 2 : 3, kAhead = kStages - 1;   // row tiles requested ahead
-  static constexpr int kPerSM = R == 16 ? 3 : (R == 32 ? 2 : 1);          // CTAs that fit
+  static constexpr int kCols = R <= 32 ? 128 : 64, kTok = 64, kOrders = 8;
+  static constexpr int kStages = R <= 64 ? 2 : 3, kAhead = kStages - 1;   // row tiles requested ahead
+  static constexpr int kPerSM = R == 16 ? 3 : (R <= 64 ? 2 : 1);          // CTAs that fit
   static constexpr int kWC = kCols / 16, kNI = R / 16 / (kWarps / kWC);   // column groups; rho tiles per warp
   static constexpr int kRowBytes = kTok * kCols * 2;
   static constexpr int kStage = kRowBytes + kTok * R * 4;     // rows, and mid in fp32
