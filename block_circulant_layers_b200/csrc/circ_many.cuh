@@ -58,9 +58,11 @@ k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T*
     prefetch_l2(base + tok.row(threadIdx.x) * (int64_t)D + (int64_t)o0 * P, QI * P * (int)sizeof(T));
   if (ad >= plan.n) {                                       // no adapter: the base row, or zeros
     if (base == out) return;
-    for (int e = threadIdx.x; e < m * QI * P; e += NT) {
-      const int64_t at = tok.row(e / (QI * P)) * D + o0 * P + e % (QI * P);
-      out[at] = base ? base[at] : from_f32<T>(0.0f);
+    for (int t = 0; t < m; ++t) {
+      const int64_t at = tok.row(t) * D + (int64_t)o0 * P;
+      for (int e = threadIdx.x * (16 / (int)sizeof(T)); e < QI * P; e += NT * (16 / (int)sizeof(T)))
+        *reinterpret_cast<uint4*>(out + at + e) =
+            base ? *reinterpret_cast<const uint4*>(base + at + e) : make_uint4(0, 0, 0, 0);
     }
     return;
   }
@@ -103,9 +105,11 @@ struct SliceWalk {
 template <int P, typename T>
 __device__ __forceinline__ void zero_unplanned(T* grad_x, const PlanView& v, int q, int j0, int QJ) {
   const int beg = __ldg(v.offsets + v.n), end = __ldg(v.offsets + v.n + 1), w = QJ * P;
-  for (int t = beg + blockIdx.x; t < end; t += gridDim.x)
-    for (int e = threadIdx.x; e < w; e += blockDim.x)
-      grad_x[(int64_t)__ldg(v.order + t) * q * P + (int64_t)j0 * P + e] = from_f32<T>(0.0f);
+  constexpr int V = 16 / (int)sizeof(T);
+  for (int t = beg + blockIdx.x; t < end; t += gridDim.x) {
+    T* const row = grad_x + (int64_t)__ldg(v.order + t) * q * P + (int64_t)j0 * P;
+    for (int e = threadIdx.x * V; e < w; e += blockDim.x * V) *reinterpret_cast<uint4*>(row + e) = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // grid: token slices x input-block groups. The sums of slice s over adapter a go to slot s + a
