@@ -2,7 +2,7 @@
 //   norm = sqrt(sum over all elements of g^2),  out = g * min(1, max_norm / (norm + 1e-6)).
 //
 // Two launches for up to kMost tensors. The elements are cut into blocks of 16384 of one tensor.
-// k_norm_partial: a CTA sums the squares of every grid-th block and stores one double;
+// k_norm_partial: a CTA sums the squares of an equal run of blocks and stores one double;
 // k_norm_finish: every CTA adds all those partial sums in the same order, so the norm is the
 // same on every run and needs no counter or zeroed state, and then scales its blocks. It takes
 // them in the opposite order: what the first pass read last is still in L2.
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFew = 64, kMost = 1024;         // tensors per launch (kernel parameters: 32764 bytes at most)
-constexpr int kMaxGrid = 592;                  // partial sums per launch
+constexpr int kMaxGrid = 1184;                 // partial sums per launch
 constexpr int kPer = 8;                        // units of 8 elements per thread and block
 constexpr int kUnits = kPer * kThreads;        // units per block
 
@@ -116,7 +116,7 @@ __device__ __forceinline__ double block_sum(double v) {
 template <bool LAST, typename Use>
 __device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, int64_t n, Use use) {
   const char* base = static_cast<const char*>(p) + e0 * (bf16 ? 2 : 4);
-  if (n - e0 < 8 * kUnits || (reinterpret_cast<uintptr_t>(base) & 15) != 0) {
+  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0) {
     for (int i = 0; i < kPer; ++i) {
       const int64_t e = e0 + 8 * (threadIdx.x + kThreads * i);
       if (e >= n) return;
@@ -126,12 +126,17 @@ __device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, 
     }
     return;
   }
+  // whole units; the one that the tensor ends in, if any, is its thread's at the end
+  const int whole = (int)min((n - e0) / 8, (int64_t)kUnits);
   const float4* src = reinterpret_cast<const float4*>(base);
-  auto get = [](const float4* a) { return LAST ? __ldcs(a) : *a; };
+  auto get = [&](int unit, int piece, int per_unit) {
+    const float4* a = src + per_unit * unit + piece;
+    return unit < whole ? (LAST ? __ldcs(a) : *a) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
   if (bf16) {
     float4 w[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) w[i] = get(src + threadIdx.x + kThreads * i);
+    for (int i = 0; i < kPer; ++i) w[i] = get(threadIdx.x + kThreads * i, 0, 1);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint32_t u[4] = {__float_as_uint(w[i].x), __float_as_uint(w[i].y), __float_as_uint(w[i].z),
@@ -142,7 +147,7 @@ __device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, 
         v[2 * k] = __uint_as_float(u[k] << 16);
         v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
       }
-      use(e0 + 8 * (threadIdx.x + kThreads * i), v);
+      if ((int)threadIdx.x + kThreads * i < whole) use(e0 + 8 * (threadIdx.x + kThreads * i), v);
     }
   } else {
 #pragma unroll
@@ -150,14 +155,21 @@ __device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, 
       float4 w[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        w[i] = get(src + 2 * (threadIdx.x + kThreads * (kPer / 2 * h + i / 2)) + (i & 1));
+        w[i] = get(threadIdx.x + kThreads * (kPer / 2 * h + i / 2), i & 1, 2);
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) {
         const float4 a = w[2 * i], b = w[2 * i + 1];
         float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        use(e0 + 8 * (threadIdx.x + kThreads * (kPer / 2 * h + i)), v);
+        const int unit = threadIdx.x + kThreads * (kPer / 2 * h + i);
+        if (unit < whole) use(e0 + 8 * unit, v);
       }
     }
+  }
+  const int64_t e = e0 + 8 * (int64_t)whole;
+  if (whole < kUnits && e < n && (int)threadIdx.x == whole % kThreads) {
+    float v[8];
+    load_unit(p, bf16, e, n, v);
+    use(e, v);
   }
 }
 
@@ -166,9 +178,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant
                                                            double* __restrict__ partial) {
   griddep_wait();
   const int64_t blocks = t.first[t.count];
+  const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
   double sum = 0.0;
-  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int i = tensor_of(t, b);
+  int i = b0 < b1 ? tensor_of(t, b0) : 0;
+  for (int64_t b = b0; b < b1; ++b) {
+    while (b >= t.first[i + 1]) ++i;
     const int64_t n = 8 * kUnits * (t.first[i + 1] - t.first[i]) - t.tail[i];
     each_unit<false>(t.in[i], t.bf16[i], 8 * kUnits * (b - t.first[i]), n, [&](int64_t, const float (&v)[8]) {
       float s = 0.0f;
@@ -200,9 +214,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_finish(const __grid_constant_
   const float ratio = max_norm / (nrm + 1e-6f);
   const float coef = ratio > 1.0f ? 1.0f : ratio;
   const int64_t blocks = t.first[t.count];
-  for (int64_t r = blockIdx.x; r < blocks; r += gridDim.x) {
-    const int64_t b = blocks - 1 - r;
-    const int i = tensor_of(t, b);
+  const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+  int i = b0 < b1 ? tensor_of(t, b1 - 1) : 0;
+  for (int64_t b = b1 - 1; b >= b0; --b) {
+    while (b < t.first[i]) --i;
     const int64_t n = 8 * kUnits * (t.first[i + 1] - t.first[i]) - t.tail[i];
     each_unit<true>(t.in[i], t.bf16[i], 8 * kUnits * (b - t.first[i]), n, [&](int64_t e, float (&v)[8]) {
 #pragma unroll

@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 template <int R>
 struct Wgrad {
   static constexpr int kCols = R <= 32 ? 128 : 64, kTok = 64, kOrders = 8;
-  static constexpr int kStages = R <= 64 ? 2 : 3, kAhead = kStages - 1;   // row tiles requested ahead
-  static constexpr int kPerSM = R == 16 ? 3 : (R <= 64 ? 2 : 1);          // CTAs that fit
+  static constexpr int kStages = R == 16 ? 3 : (R <= 64 ? 2 : 3), kAhead = kStages - 1;   // row tiles requested ahead
+  static constexpr int kPerSM = R == 16 ? 2 : (R <= 64 ? 2 : 1);          // CTAs that fit
   static constexpr int kWC = kCols / 16, kNI = R / 16 / (kWarps / kWC);   // column groups; rho tiles per warp
   static constexpr int kRowBytes = kTok * kCols * 2;
   static constexpr int kStage = kRowBytes + kTok * R * 4;     // rows, and mid in fp32

@@ -147,7 +147,8 @@ CIRC = [  # T, D, p, n, ids
     (1, 4096, 128, 2, "one"), (5, 64, 64, 1, "mixed"), (9, 320, 64, 4, "wild"), (16, 4096, 128, 16, "mixed"),
     (37, 1024, 256, 3, "none"), (60, 1536, 512, 2, "runs"), (70, 4096, 512, 3, "runs"), (33, 2048, 1024, 2, "mixed"),
     (20, 1024, 1024, 4, "mixed"), (11, 4096, 2048, 3, "mixed"), (10, 2048, 2048, 2, "one"), (6, 8192, 4096, 2, "mixed"),
-    (300, 4096, 128, 2, "runs"), (400, 1024, 128, 1, "one"), (700, 4096, 512, 5, "runs"), (333, 4096, 1024, 40, "mixed"), (280, 640, 128, 90, "mixed"), (5, 4096, 4096, 2, "one")]
+    (300, 4096, 128, 2, "runs"), (400, 1024, 128, 1, "one"), (700, 4096, 512, 5, "runs"), (333, 4096, 1024, 40, "mixed"), (280, 640, 128, 90, "mixed"), (5, 4096, 4096, 2, "one"),
+    (9, 8192, 64, 2, "mixed")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -228,7 +229,7 @@ def flat64(ts):
     return torch.cat([t.detach().double().cpu().flatten() for t in ts])
 
 
-@pytest.mark.parametrize("sizes", [[1], [5, 0, 3], [7, 8, 9, 1000, 65537], [32768] * 64, [13] * 600, [3_000_001]])
+@pytest.mark.parametrize("sizes", [[1], [5, 0, 3], [7, 8, 9, 1000, 65537], [32768] * 64, [13] * 600, [300, 0, 70000] * 500, [3_000_001]])
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "mixed"])
 def test_grad_norm_and_clip(rd, sizes, dtype):
     kinds = {"bf16": [torch.bfloat16], "f32": [torch.float32], "mixed": [torch.bfloat16, torch.float32]}[dtype]
