@@ -100,13 +100,14 @@ cudaError_t launch_circ_many_fused(const CircMany& a, int p, int dtype, cudaStre
 cudaError_t launch_circ_many_bwd(const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink);
 
 // Low-rank adapters: rows (forward: in = x, w1 = a, w2 = b; bwd: in = g, w1 = b, w2 = a) and
-// weight gradients. Arguments as lora_fwd / lora_bwd in rdfft.h.
+// weight gradients (after_rows: the rows kernel that writes v is the launch just before on s).
+// Arguments as lora_fwd / lora_bwd in rdfft.h.
 cudaError_t launch_lora_rows(bool bwd, const void* in, const void* w1, const void* w2, const float* scale,
                              const void* base, void* out, float* mid, const int* plan, int64_t T, int K, int N,
                              int r, int n, int dtype, cudaStream_t s);
 cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, const float* v, const float* scale,
-                              float* grad_a, float* grad_b, const int* plan, int64_t T, int K, int N, int r, int n,
-                              int dtype, cudaStream_t s);
+                              float* grad_a, float* grad_b, bool after_rows, const int* plan, int64_t T, int K, int N,
+                              int r, int n, int dtype, cudaStream_t s);
 
 // Reads and clears the error words of the kernels that take a plan (bit 0: a plan of other
 // sizes was given).

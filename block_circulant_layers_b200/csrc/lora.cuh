@@ -85,8 +85,14 @@ struct LoraWgrad {
   float* grad_a;
   float* grad_b;
   int K, N, r;
+  bool after_rows;         // the rows kernel that writes v is the launch just before
   PlanView plan;
 };
+
+// The part for grad_b reads nothing that the rows kernel writes, so its CTAs need not wait for
+// it: the rows kernel lets them start only after all work before it has completed. They wait
+// before they exit, so that the grid still ends after the rows kernel.
+__device__ __forceinline__ bool starts_early(bool after_rows, bool is_a) { return after_rows && !is_a; }
 
 // The weight gradients share the batch evenly: CTA `rank` of a cluster of C takes an equal part
 // [lo, hi) of the plan's 64-token tiles, whatever adapters they belong to. (A CTA per adapter

@@ -591,7 +591,7 @@ struct Wgrad {
 
 template <int R>
 __global__ void __launch_bounds__(kThreads, Wgrad<R>::kPerSM)
-k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
+k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
   using S = Wgrad<R>;
   constexpr int COLS = S::kCols, UNITS = COLS / 8, NI = S::kNI;
   constexpr int NA = NI * 8;                                   // sums per thread
@@ -601,12 +601,13 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   unsigned char* const mid_p = ring + S::kStage * S::kStages;
   float* const head = reinterpret_cast<float*>(mid_p + S::kMid);   // [NA][kThreads]
   const uint32_t ring_at = shared_at(ring), mid_at = shared_at(mid_p);
-  griddep_wait();
-  if (!plan_matches(a.plan)) return;
   const unsigned C = cluster_size(), rank = cluster_rank();
   const int r = a.r, block = blockIdx.x / C;
-  const bool is_a = block < blocks_a;
-  const int n0 = S::kCols * (is_a ? block : block - blocks_a);
+  const bool is_a = block >= blocks_b;                         // grad_b's blocks first: they start early
+  const bool early = starts_early(a.after_rows, is_a);
+  if (!early) griddep_wait();
+  if (!plan_matches(a.plan)) return;
+  const int n0 = S::kCols * (is_a ? block - blocks_b : block);
   const int W = is_a ? a.K : a.N;                              // columns of the rows read
   const bf16_t* const rows = is_a ? a.x : a.g;
   const float* const mid = is_a ? a.v : a.u;
@@ -766,6 +767,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_a) {
   for (int ad = rank; ad < a.plan.n; ad += C)
     if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
   if (C > 1) cluster_wait();                                   // the others are done with this CTA's memory
+  if (early) griddep_wait();
 }
 
 template <auto KERNEL>
@@ -795,7 +797,7 @@ cudaError_t run_wgrad(const LoraWgrad<bf16_t>& a, cudaStream_t s) {
   // by both widths, so that a gradient does not depend on whether the other is asked for
   const int cluster = lora_token_split(a.plan.T, a.plan.n, ka + nb, S::kTok, S::kPerSM);
   return launch_cluster_pdl(k_lora_wgrad<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster, S::smem, s,
-                            a, ba);
+                            a, bb);
 }
 
 template <bool BWD>

@@ -301,7 +301,7 @@ struct WgradF32 {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_a) {
+__global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f32(LoraWgrad<float> a, int blocks_b) {
   using S = WgradF32<R>;
   constexpr int RT = S::RT, TG = S::TG, NA = R * 64 / kThreads;
   extern __shared__ __align__(16) float sm[];               // ring
@@ -309,12 +309,13 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
   float* const shares = head + R * 64;                      // [TG][R][SS]
   __shared__ int2 desc[kWindow + 2];
   __shared__ __align__(16) int order[S::kOrders][S::kTok];
-  griddep_wait();
-  if (!plan_matches(a.plan)) return;
   const unsigned C = cluster_size(), rank = cluster_rank();
   const int r = a.r, tid = threadIdx.x, block = blockIdx.x / C;
-  const bool is_a = block < blocks_a;
-  const int n0 = 64 * (is_a ? block : block - blocks_a);
+  const bool is_a = block >= blocks_b;                         // grad_b's blocks first: they start early
+  const bool early = starts_early(a.after_rows, is_a);
+  if (!early) griddep_wait();
+  if (!plan_matches(a.plan)) return;
+  const int n0 = 64 * (is_a ? block - blocks_b : block);
   const int W = is_a ? a.K : a.N;
   const float* const rows = is_a ? a.x : a.g;
   const float* const mid = is_a ? a.v : a.u;
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
   for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens
     if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
   if (C > 1) cluster_wait();                                // the others are done with this CTA's memory
+  if (early) griddep_wait();
 }
 
 template <int R, int M, bool BWD>
@@ -530,7 +532,7 @@ cudaError_t run_wgrad(const LoraWgrad<float>& a, cudaStream_t s) {
   // by both widths, so that a gradient does not depend on whether the other is asked for
   const int cluster = lora_token_split(a.plan.T, a.plan.n, ka + nb, S::kTok, S::kPerSM);
   return launch_cluster_pdl(k_lora_wgrad_f32<R>, dim3((unsigned)((ba + bb) * cluster)), dim3(kThreads), cluster,
-                            S::smem, s, a, ba);
+                            S::smem, s, a, bb);
 }
 
 }  // namespace

@@ -122,24 +122,25 @@ cudaError_t launch_lora_rows(bool bwd, const void* in, const void* w1, const voi
 
 template <typename T>
 static LoraWgrad<T> wgrad_args(const void* g, const void* x, const float* u, const float* v, const float* scale,
-                               float* grad_a, float* grad_b, const int* plan, int64_t tokens, int K, int N, int r,
-                               int n) {
+                               float* grad_a, float* grad_b, bool after_rows, const int* plan, int64_t tokens, int K,
+                               int N, int r, int n) {
   LoraWgrad<T> a = {};
   a.x = static_cast<const T*>(x);
   a.g = static_cast<const T*>(g);
   a.u = u, a.v = v, a.scale = scale;
   a.grad_a = grad_a, a.grad_b = grad_b;
   a.K = K, a.N = N, a.r = r;
+  a.after_rows = after_rows;
   a.plan = plan_view(plan, tokens, n, 2);
   return a;
 }
 
 cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, const float* v, const float* scale,
-                              float* grad_a, float* grad_b, const int* plan, int64_t T, int K, int N, int r, int n,
-                              int dtype, cudaStream_t s) {
+                              float* grad_a, float* grad_b, bool after_rows, const int* plan, int64_t T, int K, int N,
+                              int r, int n, int dtype, cudaStream_t s) {
   if (dtype == 0)
-    return lora_wgrad_f32(wgrad_args<float>(g, x, u, v, scale, grad_a, grad_b, plan, T, K, N, r, n), s);
-  return lora_wgrad_bf16(wgrad_args<bf16_t>(g, x, u, v, scale, grad_a, grad_b, plan, T, K, N, r, n), s);
+    return lora_wgrad_f32(wgrad_args<float>(g, x, u, v, scale, grad_a, grad_b, after_rows, plan, T, K, N, r, n), s);
+  return lora_wgrad_bf16(wgrad_args<bf16_t>(g, x, u, v, scale, grad_a, grad_b, after_rows, plan, T, K, N, r, n), s);
 }
 
 cudaError_t take_plan_device_error(unsigned int* flags) {

@@ -422,7 +422,7 @@ int lora_bwd(const void* g, const void* x, const void* a, const void* b, const f
   cudaError_t e = cudaSuccess;
   if (rows) e = rdfft::launch_lora_rows(true, g, b, a, scale, nullptr, grad_x, v, plan, T, N, K, r, n, dtype, s);
   if (e == cudaSuccess && (grad_a || grad_b))
-    e = rdfft::launch_lora_wgrad(g, x, u, v, scale, grad_a, grad_b, plan, T, K, N, r, n, dtype, s);
+    e = rdfft::launch_lora_wgrad(g, x, u, v, scale, grad_a, grad_b, rows, plan, T, K, N, r, n, dtype, s);
   return finish(e);
 }
 
