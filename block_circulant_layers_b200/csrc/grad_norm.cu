@@ -1,13 +1,13 @@
 // Global norm of many tensors, and the tensors clipped by it:
 //   norm = sqrt(sum over all elements of g^2),  out = g * min(1, max_norm / (norm + 1e-6)).
 //
-// Two launches for up to kMost tensors. The elements are cut into blocks of 16384 of one tensor.
+// Two launches for up to kMost tensors. The elements are cut into blocks of 8192 of one tensor.
 // k_norm_partial: a CTA sums the squares of an equal run of blocks and stores one double;
 // k_norm_finish: every CTA adds all those partial sums in the same order, so the norm is the
 // same on every run and needs no counter or zeroed state, and then scales its blocks. It takes
 // them in the opposite order: what the first pass read last is still in L2.
 // Bound by memory: 1 read for the norm, 1 read and 1 write for the scaling, less what L2 keeps.
-// A thread requests its 8 pieces of 16 bytes (16 in fp32) of a block before it uses the first.
+// A thread requests its 4 pieces of 16 bytes (8 in fp32) of a block before it uses the first.
 //
 // Squares of 8 elements are added in fp32 and those sums in double, so neither long sums nor
 // many tensors lose bits; a sum of 8 that overflows fp32 or falls to its smallest range is
@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFew = 64, kMost = 1024;         // tensors per launch (kernel parameters: 32764 bytes at most)
-constexpr int kMaxGrid = 1184;                 // partial sums per launch
-constexpr int kPer = 8;                        // units of 8 elements per thread and block
+constexpr int kMaxGrid = 2368;                 // CTAs, and partial sums, per launch (four waves of 4 per SM)
+constexpr int kPer = 4;                        // units of 8 elements per thread and block
 constexpr int kUnits = kPer * kThreads;        // units per block
 
 // One launch's tensors: tensor i has the blocks [first[i], first[i + 1]), and its last block
@@ -150,19 +150,15 @@ __device__ __forceinline__ void each_unit(const void* p, bool bf16, int64_t e0, 
       if ((int)threadIdx.x + kThreads * i < whole) use(e0 + 8 * (threadIdx.x + kThreads * i), v);
     }
   } else {
+    float4 w[2 * kPer];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float4 w[kPer];
+    for (int i = 0; i < 2 * kPer; ++i) w[i] = get(threadIdx.x + kThreads * (i / 2), i & 1, 2);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        w[i] = get(threadIdx.x + kThreads * (kPer / 2 * h + i / 2), i & 1, 2);
-#pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) {
-        const float4 a = w[2 * i], b = w[2 * i + 1];
-        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const int unit = threadIdx.x + kThreads * (kPer / 2 * h + i);
-        if (unit < whole) use(e0 + 8 * unit, v);
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const float4 a = w[2 * i], b = w[2 * i + 1];
+      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      const int unit = threadIdx.x + kThreads * i;
+      if (unit < whole) use(e0 + 8 * unit, v);
     }
   }
   const int64_t e = e0 + 8 * (int64_t)whole;
