@@ -380,56 +380,77 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   const int K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
 
-  // this CTA's steps of COLS columns: [0, n1) of in and w1, then [n1, n1 + n2) of base and w2
+  // this CTA's steps of COLS columns, every C-th (the cluster reads a row's columns side by side):
+  // [0, n1) of in and w1, then [n1, n1 + n2) of base and w2
   const int ks = (K + COLS - 1) / COLS, ns = (N + COLS - 1) / COLS;
-  const int k_first = (int)((int64_t)ks * rank / C), n_first = (int)((int64_t)ns * rank / C);
-  const int n1 = adapted ? (int)((int64_t)ks * (rank + 1) / C) - k_first : 0;
-  const int n2 = (a.out != nullptr && (adapted || a.base != a.out)) ? (int)((int64_t)ns * (rank + 1) / C) - n_first : 0;
+  const auto mine = [&](int all) { return (all - (int)rank + (int)C - 1) / (int)C; };
+  const int n1 = adapted ? mine(ks) : 0;
+  const int n2 = (a.out != nullptr && (adapted || a.base != a.out)) ? mine(ns) : 0;
   const bf16_t* const w1 = a.w1 + (adapted ? (int64_t)ad * r * K : 0);
   const bf16_t* const w2 = a.w2 + (adapted ? (int64_t)ad * r * N : 0);
-  // a thread moves one unit of every ROWS-th row of a row tile
+  // A thread moves one unit of every ROWS-th row of a row tile, and WL units of a weight tile:
+  // r rows of COLS columns (w1 forward, w2 backward), or COLS rows of r columns. Its addresses go
+  // from step to step by a fixed distance. Rows beyond the tile's tokens are left as they are:
+  // they reach only their own rows of the products, which nobody stores.
+  constexpr int WL = (UNITS * R + kThreads - 1) / kThreads;
   const int trow = tid / UNITS, tunit = tid % UNITS;
   int tok[NH];
 #pragma unroll
   for (int h = 0; h < NH; ++h) tok[h] = trow + ROWS * h < m ? __ldg(a.plan.order + pos0 + trow + ROWS * h) : -1;
-
-  auto request = [&](int step) {
-    if (step < n1 + n2) {
-      const bool first = step < n1;
-      const int c0 = COLS * (first ? k_first + step : n_first + step - n1), W = first ? K : N;
-      const bf16_t* const rows = first ? a.in : a.base;
-      const uint32_t dst = ring_at + step % S::kStages * S::kStage;
-      const int c = c0 + 8 * tunit;
+  const uint32_t x_dst = ring_at + at<COLS>(trow, tunit);
+  const bf16_t *px[NH], *pw[WL];
+  uint32_t w_dst[WL];
+  int64_t w_go;                                                // per step, in elements
+  int rcol, wcol[WL];                                          // columns the next request begins with
+  bool w_in[WL];
+  int rstep = 0, rslot = 0, RW;
+  auto aim = [&](bool first) {                                 // at the first step of a half
+    const bf16_t* const rows = first || a.base == nullptr ? a.in : a.base;
+    const bf16_t* const w = first ? w1 : w2;
+    const bool along = first != BWD;
+    RW = first ? K : N;
+    rcol = COLS * (int)rank + 8 * tunit;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const bool in = rows != nullptr && tok[h] >= 0 && c < W;
-        cp16(dst + at<COLS>(trow + ROWS * h, tunit), in ? rows + (int64_t)tok[h] * W + c : a.in, in);
-      }
-      if (adapted) {
-        const bf16_t* const w = first ? w1 : w2;
-        const uint32_t wdst = dst + S::kRowBytes;
-        // r rows of COLS columns (w1 forward, w2 backward), or COLS rows of r columns
-        const bool along = first != BWD;
+    for (int h = 0; h < NH; ++h) px[h] = rows + (int64_t)max(tok[h], 0) * RW + rcol;
+    w_go = (int64_t)COLS * C * (along ? 1 : r);
 #pragma unroll
-        for (int i = 0; i < (UNITS * R + kThreads - 1) / kThreads; ++i) {
-          const int e = tid + kThreads * i;
-          if (UNITS * R < kThreads && e >= UNITS * R) break;
-          if (along) {
-            const int rho = e / UNITS, cc = c0 + e % UNITS * 8;
-            const bool in = rho < r && cc < W;
-            cp16(wdst + at<COLS>(rho, e % UNITS), in ? w + (int64_t)rho * W + cc : w, in);
-          } else {
-            const int cr = e / (R / 8), u = e % (R / 8);
-            const bool in = c0 + cr < W && 8 * u < r;
-            cp16(wdst + at<R>(cr, u), in ? w + (int64_t)(c0 + cr) * r + 8 * u : w, in);
-          }
+    for (int i = 0; i < WL; ++i) {
+      const int e = tid + kThreads * i;
+      const int rho = along ? e / UNITS : e % (R / 8) * 8, c = along ? e % UNITS * 8 : e / (R / 8);
+      wcol[i] = COLS * (int)rank + c;
+      w_in[i] = rho < r;
+      pw[i] = along ? w + (int64_t)rho * RW + wcol[i] : w + (int64_t)wcol[i] * r + rho;
+      w_dst[i] = ring_at + S::kRowBytes + (along ? at<COLS>(rho, c / 8) : at<R>(c, rho / 8));
+    }
+  };
+  auto request = [&] {
+    if (rstep < n1 + n2) {
+      if (rstep == n1) aim(false);
+      const uint32_t slot = rslot * S::kStage;
+      if (rstep < n1 || a.base != nullptr) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (tok[h] >= 0) cp16(x_dst + slot + h * ROWS * COLS * 2, px[h], rcol < RW);
+          px[h] += COLS * C;
         }
       }
+      if (adapted) {
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+          if (UNITS * R >= kThreads || tid < UNITS * R) cp16(w_dst[i] + slot, pw[i], w_in[i] && wcol[i] < RW);
+          pw[i] += w_go;
+          wcol[i] += COLS * C;
+        }
+      }
+      rcol += COLS * C;
+      ++rstep;
+      rslot = rslot + 1 == S::kStages ? 0 : rslot + 1;
     }
     cp_commit();
   };
+  if (n1 > 0) aim(true);
 #pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) request(s);
+  for (int s = 0; s < S::kStages - 1; ++s) request();
 
   const int wm = warp % 4, wh = warp / 4;                      // 16 rows; half of a step's columns
   // fragment offsets: rows of in or base; w1; mid; w2
@@ -437,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   const uint32_t w1_off = BWD ? lane_rows<R>(lane) : lane_cols<COLS>(lane);
   const uint32_t mid_off = moved<R>(lane_rows<R>(lane), 16 * wm, 0);
   const uint32_t w2_off = BWD ? lane_rows<COLS>(lane) : lane_cols<R>(lane);
+  int slot = 0;                                                // stage of the step at hand
   if (adapted) {
     float acc[R / 8][4];
 #pragma unroll
@@ -446,8 +468,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
     for (int step = 0; step < n1; ++step) {
       cp_wait<S::kStages - 2>();
       __syncthreads();
-      request(step + S::kStages - 1);
-      const uint32_t x_at = ring_at + step % S::kStages * S::kStage, w_at = x_at + S::kRowBytes;
+      request();
+      const uint32_t x_at = ring_at + slot * S::kStage, w_at = x_at + S::kRowBytes;
+      slot = slot + 1 == S::kStages ? 0 : slot + 1;
 #pragma unroll
       for (int k = COLS / 2 * wh; k < COLS / 2 * (wh + 1); k += 16) {
         uint32_t x[4];
@@ -511,12 +534,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   for (int step = n1; step < n1 + n2; ++step) {
     cp_wait<S::kStages - 2>();
     __syncthreads();                                           // the stage, and at first mid, is complete
-    request(step + S::kStages - 1);
-    unsigned char* const tile_p = ring + step % S::kStages * S::kStage;
-    const uint32_t w_at = ring_at + step % S::kStages * S::kStage + S::kRowBytes;
+    request();
+    unsigned char* const tile_p = ring + slot * S::kStage;
+    const uint32_t out_at = ring_at + slot * S::kStage, w_at = out_at + S::kRowBytes;
+    slot = slot + 1 == S::kStages ? 0 : slot + 1;
     if (adapted) {
       // the sums start from base, whose fragments lie in the stage as the results will
-      const uint32_t out_at = ring_at + step % S::kStages * S::kStage;
       float acc[COLS / 16][4];
 #pragma unroll
       for (int j = 0; j < COLS / 32; ++j) {
@@ -554,12 +577,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
       }
       __syncthreads();
     }
-    const int c = COLS * (n_first + step - n1) + 8 * tunit;
+    const int c = COLS * ((int)rank + (int)C * (step - n1)) + 8 * tunit;
 #pragma unroll
     for (int h = 0; h < NH; ++h)
       if (tok[h] >= 0 && c < N)
         *reinterpret_cast<uint4*>(a.out + (int64_t)tok[h] * N + c) =
-            *reinterpret_cast<const uint4*>(tile_p + at<COLS>(trow + ROWS * h, tunit));
+            adapted || a.base != nullptr
+                ? *reinterpret_cast<const uint4*>(tile_p + at<COLS>(trow + ROWS * h, tunit))
+                : make_uint4(0, 0, 0, 0);
   }
   cp_wait<0>();
   if (adapted && C > 1) cluster_wait();                        // the others are done with this CTA's memory
