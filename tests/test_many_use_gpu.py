@@ -190,6 +190,24 @@ def test_training_step_of_both_kinds(rd, dtype):
         assert float((g - b * coef).abs().max()) <= 1e-6 * float(b.abs().max())
 
 
+def test_readme_example(rd):
+    """The example runs, and its parameters get finite gradients, of the adapters in use only."""
+    import os
+    import re
+
+    from conftest import ROOT
+    with open(os.path.join(ROOT, "README.md")) as f:
+        code = re.findall(r"```python\n(.*?)```", f.read(), flags=re.S)
+    assert len(code) == 1
+    scope = {}
+    exec(code[0], scope)                                                     # noqa: S102
+    low, circ, ids = scope["low"], scope["circ"], scope["ids"]
+    assert set(ids.tolist()) == {-1, 0, 1} and bool(torch.isfinite(scope["norm"]))
+    for t in (low.b.grad, circ.c.grad):
+        assert bool(torch.isfinite(t).all()) and bool(t.flatten(1).any(1).all())
+    assert not bool(low.a.grad.any())                                        # b starts at zero
+
+
 def test_bucket_clip(rd):
     from block_circulant_layers_b200.dp import GradCBucket
     bucket = GradCBucket([torch.Size((2, 2, 64)), torch.Size((3,)), torch.Size((4, 4, 128))], "cuda")
