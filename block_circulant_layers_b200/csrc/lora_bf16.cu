@@ -596,12 +596,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 }
 
 // ------------------------------------------------------------------- weight gradients
-// One cluster: 128 (64 at r > 32) columns of x (grad_a) or of g (grad_b) over all tokens, its CTAs sharing the
-// plan's 64-token tiles evenly (TileShare). D[rho, column] = sum_t mid[t, rho] row[t, column]:
-// tokens are the contraction index, and both operands are read transposed. A warp has 16
-// columns and every rho (half of them at r > 32), so no sums are shared inside a CTA. An adapter whose tiles lie in
-// several CTAs is written by the first of them, which adds the others' sums in rank order
-// through distributed shared memory.
+// One cluster: 128 (64 at r > 32) columns of x (grad_a) or of g (grad_b) over all tokens, its
+// CTAs sharing the plan's 64-token tiles evenly (TileShare). D[rho, column] = sum_t mid[t, rho]
+// row[t, column]: tokens are the contraction index, and both operands are read transposed. A
+// warp has 16 columns and every rho (half of them at r > 32), so no sums are shared inside a
+// CTA. An adapter whose tiles lie in several CTAs is written by the first of them, which adds
+// the others' sums in rank order through distributed shared memory.
 // Tiles pass through a ring of cp.async stages: a tile's rows are requested one or two steps
 // ahead, its token numbers two steps before that.
 // mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits

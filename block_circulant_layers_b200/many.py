@@ -111,7 +111,7 @@ class LowRankAdapters(torch.nn.Module):
                                                  device=device))
 
     def forward(self, x: torch.Tensor, plan: _b.AdapterPlan, base: torch.Tensor | None = None) -> torch.Tensor:
-        return low_rank_many(x, self.a, self.b, plan, self.scale, base)
+        return low_rank_many(x, self.a, self.b, plan, self.scale.float(), base)
 
     def extra_repr(self) -> str:
         n, r, K = self.a.shape

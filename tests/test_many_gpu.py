@@ -60,7 +60,9 @@ LORA = [  # T, K, N, r, n, ids
     (1, 4096, 4096, 16, 4, "one"), (1, 8, 8, 8, 1, "mixed"), (7, 40, 264, 8, 3, "none"), (16, 256, 4096, 64, 16, "mixed"),
     (33, 1032, 520, 24, 5, "wild"), (64, 4096, 1024, 128, 3, "mixed"), (100, 520, 72, 40, 200, "mixed"),
     (300, 2056, 1000, 16, 2, "runs"), (500, 1024, 2048, 128, 4, "runs"), (1000, 96, 8200, 32, 1, "one"),
-    (257, 4104, 120, 64, 3, "runs"), (129, 72, 64, 112, 1, "wild"), (65, 64, 8, 48, 1, "one")]
+    (257, 4104, 120, 64, 3, "runs"), (129, 72, 64, 112, 1, "wild"), (65, 64, 8, 48, 1, "one"),
+    (150000, 64, 72, 8, 3, "runs"), (2000, 320, 4096, 64, 7, "mixed"), (3000, 1000, 264, 16, 700, "wild"),
+    (1100, 136, 2056, 128, 30, "runs")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -131,6 +131,21 @@ def test_modules_skip_what_needs_no_gradient(rd):
         assert not bank(x, plan).requires_grad
 
 
+def test_modules_in_bf16_and_without_tokens(rd):
+    n, K, r = 2, 64, 8
+    bank = rd.LowRankAdapters(n, K, K, r, device="cuda").to(torch.bfloat16)
+    with torch.no_grad():
+        bank.b.copy_(randn(3, n, K, r))
+    plan = rd.adapter_plan(make_ids("mixed", 20, n).cuda(), n)
+    bank(randn(1, 20, K, dtype=torch.bfloat16), plan).float().square().sum().backward()
+    assert bank.a.grad.dtype == bank.b.grad.dtype == torch.bfloat16 and bool(bank.b.grad.any())
+    empty = rd.adapter_plan(torch.empty(0, dtype=torch.int32, device="cuda"), n)
+    x = torch.empty(0, K, device="cuda", requires_grad=True)
+    for bank in (rd.LowRankAdapters(n, K, K, r, device="cuda"), rd.BlockCirculantAdapters(n, K, 64, device="cuda")):
+        bank(x, empty).sum().backward()
+        assert x.grad.shape == (0, K) and all(not bool(p.grad.any()) for p in bank.parameters())
+
+
 def test_a_plan_made_again_fails_the_backward(rd):
     n, K, T = 2, 64, 16
     ids = make_ids("mixed", T, n).cuda()
