@@ -534,8 +534,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
       if ((unsigned)(t % C) == rank) a.mid[(int64_t)__ldg(a.plan.order + pos0 + t) * r + e % r] = 0.0f;
     }
   }
-  griddep_launch_dependents();
-
   for (int step = n1; step < n1 + n2; ++step) {
     cp_wait<S::kStages - 2>();
     __syncthreads();                                           // the stage, and at first mid, is complete
@@ -591,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
                 ? *reinterpret_cast<const uint4*>(tile_p + at<COLS>(trow + ROWS * h, tunit))
                 : make_uint4(0, 0, 0, 0);
   }
+  griddep_launch_dependents();
   cp_wait<0>();
   if (adapted && C > 1) cluster_wait();                        // the others are done with this CTA's memory
 }
