@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 // warp has 16 columns and every rho (half of them at r > 32), so no sums are shared inside a
 // CTA. An adapter whose tiles lie in several CTAs is written by the first of them, which adds
 // the others' sums in rank order through distributed shared memory.
-// Tiles pass through a ring of cp.async stages: a tile's rows are requested one or two steps
-// ahead, its token numbers two steps before that.
+// Tiles pass through a ring of cp.async stages: a tile's rows are requested one to three
+// steps ahead, its token numbers two or three steps before that.
 // mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits
 // (24 mantissa bits), since the gradients are fp32.
 // K = N = 4096, r = 16, 4096 tokens: 22.3 us for the 67 MB of x and g (3.0 TB/s; shared-memory
@@ -611,8 +611,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 template <int R>
 struct Wgrad {
   static constexpr int kCols = R <= 32 ? 128 : 64, kTok = 64, kOrders = 8;
-  static constexpr int kStages = R == 16 ? 3 : (R <= 64 ? 2 : 3), kAhead = kStages - 1;   // row tiles requested ahead
-  static constexpr int kPerSM = R == 16 ? 2 : (R <= 64 ? 2 : 1);          // CTAs that fit
+  static constexpr int kStages = R == 16 ? 4 : (R == 64 ? 2 : 3), kAhead = kStages - 1;   // row tiles requested ahead
+  // A tile's token numbers come with the rows of the tile kOrder before it, which have arrived
+  // when its own rows are requested (kOrder >= kAhead).
+  static constexpr int kOrder = kAhead < 2 ? 2 : kAhead;
+  static_assert(kAhead + kOrder < kOrders, "order ring");
+  static constexpr int kPerSM = R <= 64 ? 2 : 1;              // CTAs that fit
   static constexpr int kWC = kCols / 16, kNI = R / 16 / (kWarps / kWC);   // column groups; rho tiles per warp
   static constexpr int kRowBytes = kTok * kCols * 2;
   static constexpr int kStage = kRowBytes + kTok * R * 4;     // rows, and mid in fp32
@@ -711,15 +715,15 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
         }
       }
     };
-    request_order(0);
-    request_order(1);
+#pragma unroll
+    for (int s = 0; s < S::kOrder; ++s) request_order(s);
     cp_commit();
     cp_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < S::kAhead; ++s) {
       request(s);
-      request_order(s + 2);
+      request_order(s + S::kOrder);
       cp_commit();
     }
     if (w0 == share.lo) from_before = desc[0].y == desc[1].y;
@@ -727,7 +731,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
       cp_wait<S::kAhead - 1>();                                // rows i and order i + kAhead have arrived
       __syncthreads();
       request(i + S::kAhead);
-      request_order(i + S::kAhead + 2);
+      request_order(i + S::kAhead + S::kOrder);
       cp_commit();
       const unsigned char* const stage = ring + i % S::kStages * S::kStage;
 #pragma unroll
