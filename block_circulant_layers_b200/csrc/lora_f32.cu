@@ -135,11 +135,15 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
     // ---- mid = in w1^T: 4 rows x RT values per thread, rows 4 rg + i, values cg + 16 j (backward RT cg + j)
     constexpr int GT = 4 * M;                               // threads of one k group
     const int kg = tid / GT, rg = tid % GT / 16, cg = tid % 16;
-    float acc[4][RT];
+    // sums on packed fp32 pairs: the even and the odd contraction indices (added at the end), or,
+    // backward with several values of r per thread, which lie side by side, two of those
+    constexpr bool PAIR_R = BWD && RT > 1;
+    constexpr int PJ = PAIR_R ? RT / 2 : RT;
+    f2 acc[4][PJ];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
+      for (int j = 0; j < PJ; ++j) acc[i][j] = f2_bc(0.0f);
     for (int step = 0; step < n1; ++step) {
       cp_wait<S::kStages - 2>();
       __syncthreads();
@@ -159,8 +163,18 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j] = fmaf(xr[i][e], wr[e], acc[i][j]);
+              for (int e = 0; e < 4; e += 2)
+                acc[i][j] = f2_fma(f2_mk(xr[i][e], xr[i][e + 1]), f2_mk(wr[e], wr[e + 1]), acc[i][j]);
           }
+        } else if constexpr (!PAIR_R) {
+          float wr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) wr[e] = ws[(k + e) * S::W1S + cg];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              acc[i][0] = f2_fma(f2_mk(xr[i][e], xr[i][e + 1]), f2_mk(wr[e], wr[e + 1]), acc[i][0]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -169,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(xr[i][e], wr[j], acc[i][j]);
+              for (int j = 0; j < PJ; ++j)
+                acc[i][j] = f2_fma(f2_bc(xr[i][e]), f2_mk(wr[(2 * j) % RT], wr[(2 * j + 1) % RT]), acc[i][j]);
           }
         }
       }
@@ -177,7 +192,9 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) part[(kg * M + 4 * rg + i) * R + (BWD ? RT * cg + j : cg + 16 * j)] = acc[i][j];
+      for (int j = 0; j < RT; ++j)
+        part[(kg * M + 4 * rg + i) * R + (BWD ? RT * cg + j : cg + 16 * j)] =
+            PAIR_R ? (j & 1 ? acc[i][(j / 2) % PJ].y : acc[i][(j / 2) % PJ].x) : acc[i][j % PJ].x + acc[i][j % PJ].y;
     __syncthreads();
     if constexpr (S::KG > 1) {
       for (int e = tid; e < M * R; e += kThreads) {
@@ -222,14 +239,20 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   for (int i = 0; i < RM; ++i) otok[i] = RM * rg + i < m ? __ldg(a.plan.order + pos0 + RM * rg + i) : -1;
   for (int step = n1; step < n1 + n2; ++step) {
     const int n0 = kNC * (n_first + step - n1);
-    float acc[RM][4];
+    // as above: forward pairs of even and odd contraction indices, backward pairs of columns
+    constexpr int PJ = BWD ? 2 : 4;
+    float b[RM][4];
+    f2 acc[RM][PJ];
 #pragma unroll
-    for (int i = 0; i < RM; ++i)
+    for (int i = 0; i < RM; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = n0 + (BWD ? 4 * cg + j : cg + 16 * j);
-        acc[i][j] = (a.base && otok[i] >= 0 && c < N) ? a.base[(int64_t)otok[i] * N + c] : 0.0f;
+        b[i][j] = (a.base && otok[i] >= 0 && c < N) ? a.base[(int64_t)otok[i] * N + c] : 0.0f;
       }
+#pragma unroll
+      for (int j = 0; j < PJ; ++j) acc[i][j] = f2_bc(0.0f);
+    }
     cp_wait<S::kStages - 2>();
     __syncthreads();                                        // the stage, and at first mid, is complete
     request(step + S::kStages - 1);
@@ -248,7 +271,8 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 #pragma unroll
             for (int i = 0; i < RM; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j] = fmaf(mr[i][e], wr[e], acc[i][j]);
+              for (int e = 0; e < 4; e += 2)
+                acc[i][j % PJ] = f2_fma(f2_mk(mr[i][e], mr[i][e + 1]), f2_mk(wr[e], wr[e + 1]), acc[i][j % PJ]);
           }
         } else {
 #pragma unroll
@@ -258,7 +282,8 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 #pragma unroll
             for (int i = 0; i < RM; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mr[i][e], wr[j], acc[i][j]);
+              for (int j = 0; j < PJ; ++j)
+                acc[i][j] = f2_fma(f2_bc(mr[i][e]), f2_mk(wr[(2 * j) % 4], wr[(2 * j + 1) % 4]), acc[i][j]);
           }
         }
       }
@@ -269,11 +294,12 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
       float* const o = a.out + (int64_t)otok[i] * N + n0;
       if constexpr (BWD) {
         if (n0 + 4 * cg < N)
-          *reinterpret_cast<float4*>(o + 4 * cg) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          *reinterpret_cast<float4*>(o + 4 * cg) = make_float4(b[i][0] + acc[i][0].x, b[i][1] + acc[i][0].y,
+                                                               b[i][2] + acc[i][1].x, b[i][3] + acc[i][1].y);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (n0 + cg + 16 * j < N) o[cg + 16 * j] = acc[i][j];
+          if (n0 + cg + 16 * j < N) o[cg + 16 * j] = b[i][j] + (acc[i][j % PJ].x + acc[i][j % PJ].y);
       }
     }
   }
@@ -323,13 +349,14 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
   const float* const mid = is_a ? a.v : a.u;
   const int tg = tid / (kThreads / TG), cg = tid % 16, rg = tid % (kThreads / TG) / 16;
   const TileShare share(a.plan, rank, C);
-  float acc[4][RT];
+  f2 accp[2][RT];                                           // packed pairs of columns
   auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = 0.0f;
+      for (int j = 0; j < RT; ++j) accp[i][j] = f2_bc(0.0f);
   };
+  auto acc_at = [&](int i, int j) { return i & 1 ? accp[i / 2][j].y : accp[i / 2][j].x; };
   // The complete sums, four consecutive elements of the gradient (columns for grad_a, r for
   // grad_b) at a time: sum[4 v..] belongs at (rho, c) and after. One share: the register tile as
   // it is. Several: values of all of them, added in order through shared memory.
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
-          const float v = acc[i][j];
+          const float v = acc_at(i, j);
           if (is_a) sum[4 * j + i] = v;
           else sum[RT * i + j] = v;
         }
@@ -360,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
 #pragma unroll
       for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[(RT * rg + j) * S::SS + 4 * cg + i] = acc[i][j];
+        for (int i = 0; i < 4; ++i) to[(RT * rg + j) * S::SS + 4 * cg + i] = acc_at(i, j);
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < NA / 4; ++v) {
@@ -453,9 +480,11 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
         lds<4>(xs + k * S::XS + 4 * cg, xr);
         lds<RT>(ws + k * S::WS + RT * rg, wr);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int j = 0; j < RT; ++j) acc[x][j] = fmaf(xr[x], wr[j], acc[x][j]);
+        for (int j = 0; j < RT; ++j) {
+          const f2 w = f2_bc(wr[j]);
+          accp[0][j] = f2_fma(f2_mk(xr[0], xr[1]), w, accp[0][j]);
+          accp[1][j] = f2_fma(f2_mk(xr[2], xr[3]), w, accp[1][j]);
+        }
       }
       if (ends) {
         collect();
