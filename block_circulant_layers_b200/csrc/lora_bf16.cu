@@ -19,7 +19,7 @@
 //    and two cluster barriers; 5 MB would take 0.8).
 //  * k_lora_rows64: steps of 64 or 128 columns of rows and weights through a ring of cp.async
 //    stages, the second half's steps (base, w2) requested while the cluster adds up the first
-//    half's (K = N = 4096, r = 16, 4096 tokens of 8 adapters: 22.2 us, 4.6 TB/s of the 103 MB;
+//    half's (K = N = 4096, r = 16, 4096 tokens of 8 adapters: 21.6 us, 4.8 TB/s of the 103 MB;
 //    with fragments straight from global memory, as above, 39: eight warps of 142 registers per
 //    SM kept too little in flight; r = 64: 38 us).
 #include "lora.cuh"
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 // steps ahead, its token numbers two or three steps before that.
 // mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits
 // (24 mantissa bits), since the gradients are fp32.
-// K = N = 4096, r = 16, 4096 tokens: 22.3 us for the 67 MB of x and g (3.0 TB/s; shared-memory
-// latency and the two barriers of a tile), r = 64 55 us. A CTA per adapter and column group,
+// K = N = 4096, r = 16, 4096 tokens: 21.4 us for the 67 MB of x and g (about 8 us of start and
+// end, the tiles between them near the copy rate), r = 64 54 us. A CTA per adapter and column group,
 // whatever the group's size, took 41 us on uneven groups (r = 16).
 template <int R>
 struct Wgrad {

@@ -3,8 +3,9 @@
 // with the products as fp32 FMAs on register tiles fed from shared memory: the parity bar of
 // fp32 leaves no room for tf32 operands. Steps of 32 or 64 contraction indices, then of 64
 // output columns, pass through one ring of cp.async stages; operands keep their own row order, padded
-// by 16 bytes a row, and are read 4 contraction indices at a time. Shared-memory reads bound
-// it: K = N = 2048, r = 16, 4096 tokens 41.7 us forward (101 MB: 15 us); r = 64 at K = N = 4096 160 us (27 TFLOP/s).
+// by 16 bytes a row, and are read 4 contraction indices at a time; sums are kept on packed fp32
+// pairs. Shared-memory reads and their latency bound it: K = N = 2048, r = 16, 4096 tokens 39.2 us
+// forward (101 MB: 15 us); K = N = 4096, r = 64 157 us (27 TFLOP/s).
 #include "lora.cuh"
 
 #include "many_policy.h"
