@@ -443,12 +443,11 @@ k_circ_bwd_fused(const T* __restrict__ g, const T* __restrict__ x, const float* 
 }
 
 // The same for a batch of n adapters (circ_many.cuh): slice blockIdx.x takes an equal part of
-// the sorted positions that have an adapter, adapter by adapter, and stores each one's sums in
-// slot (slice + adapter) of `slots`, which no other slice and adapter share.
+// the sorted positions that have an adapter, adapter by adapter (SliceWalk).
 template <int P, int Q, int QJ, typename T, int NT, int TT, int RI, int RJ>
 __global__ void __launch_bounds__(NT, 1)
 k_circ_many_fused(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
-                  T* __restrict__ grad_x, float* __restrict__ slots, PlanView plan) {
+                  T* __restrict__ grad_x, float* grad_c, float* slots, PlanView plan) {
   using SM = FusedSmem<P, Q, QJ, T, TT>;
   constexpr int COLS = FusedShape<P, Q, QJ, NT, RI, RJ>::COLS;
   extern __shared__ float tile[];
@@ -470,7 +469,7 @@ k_circ_many_fused(const T* __restrict__ g, const T* __restrict__ x, const float*
   while (walk.next(plan)) {
     if (!fused_segment<P, Q, QJ, T, NT, TT, RI, RJ>(
             g, x, chat + (int64_t)walk.ad * Q * Q * P, grad_x,
-            slots + ((int64_t)blockIdx.x + walk.ad) * Q * Q * P, true, rows, walk.beg, walk.end, tmem_holder, phase, false))
+            walk.sums(grad_c, slots, (int64_t)Q * Q * P), true, rows, walk.beg, walk.end, tmem_holder, phase, false))
       break;
     __syncthreads();                                 // the segment's last tile and staging are consumed
   }
@@ -640,14 +639,14 @@ k_circ_bwd_small(const T* __restrict__ g, const T* __restrict__ x, const float* 
 template <int P, int Q, typename T, int NT, int TT>
 __global__ void __launch_bounds__(NT, 1)
 k_circ_many_small(const T* __restrict__ g, const T* __restrict__ x, const float* __restrict__ chat,
-                  T* __restrict__ grad_x, float* __restrict__ slots, PlanView plan) {
+                  T* __restrict__ grad_x, float* grad_c, float* slots, PlanView plan) {
   griddep_wait();
   if (!plan_matches(plan)) return;
   const PlannedPositions rows{plan.order};
   SliceWalk walk(plan);
   while (walk.next(plan)) {
     small_segment<P, Q, T, NT, TT>(g, x, chat + (int64_t)walk.ad * Q * Q * P, grad_x,
-                                   slots + ((int64_t)blockIdx.x + walk.ad) * Q * Q * P, true, rows, walk.beg, walk.end);
+                                   walk.sums(grad_c, slots, (int64_t)Q * Q * P), true, rows, walk.beg, walk.end);
     __syncthreads();                                 // the segment's last tile is consumed
   }
   zero_unplanned<P>(grad_x, plan, Q, 0, Q);
@@ -684,8 +683,8 @@ cudaError_t run_many_fused(const CircMany& a, const void* g, void* grad_x, cudaS
   const cudaError_t e = set_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)slices, (unsigned)NJG), dim3(NT), smem, s, static_cast<const T*>(g),
-                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), sink->partial,
-                    plan_view(a.plan, a.T, a.n, 0));
+                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), a.grad_c,
+                    sink->partial, plan_view(a.plan, a.T, a.n, 0));
 }
 
 template <int P, int Q, typename T, int NT, int TT>
@@ -697,8 +696,8 @@ cudaError_t run_many_small(const CircMany& a, const void* g, void* grad_x, cudaS
   const cudaError_t e = set_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)slices), dim3(NT), smem, s, static_cast<const T*>(g),
-                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), sink->partial,
-                    plan_view(a.plan, a.T, a.n, 0));
+                    static_cast<const T*>(a.in), a.c_hat, static_cast<T*>(grad_x), a.grad_c,
+                    sink->partial, plan_view(a.plan, a.T, a.n, 0));
 }
 
 // The instances of fused_t, over a plan.

@@ -83,6 +83,7 @@ k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T*
 struct SliceWalk {
   int64_t pos, hi, beg, end;                                // [beg, end): tokens of adapter ad
   int ad;
+  bool whole;                                               // all of them
   __device__ __forceinline__ explicit SliceWalk(const PlanView& v) {
     const int64_t tokens = __ldg(v.offsets + v.n);
     const int64_t slices = min((int64_t)gridDim.x, tokens);
@@ -93,14 +94,23 @@ struct SliceWalk {
     }
     beg = end = pos;
     ad = 0;
+    whole = false;
   }
   __device__ __forceinline__ bool next(const PlanView& v) {
     if (pos >= hi) return false;
     ad = __ldg(v.group + pos);
     beg = pos;
-    end = min((int64_t)__ldg(v.offsets + ad + 1), hi);
+    const int64_t all = __ldg(v.offsets + ad + 1);
+    end = min(all, hi);
+    whole = end == all && beg == __ldg(v.offsets + ad);
     pos = end;
     return true;
+  }
+  // Where the sums over this piece go, `floats` of them: the gradient itself for a whole adapter,
+  // else slot (slice + adapter). In the order of the positions each next piece has a larger
+  // slice, adapter or both, so no two share a slot.
+  __device__ __forceinline__ float* sums(float* grad_c, float* slots, int64_t floats) const {
+    return whole ? grad_c + ad * floats : slots + ((int64_t)blockIdx.x + ad) * floats;
   }
 };
 
@@ -115,17 +125,16 @@ __device__ __forceinline__ void zero_unplanned(T* grad_x, const PlanView& v, int
   }
 }
 
-// grid: token slices x input-block groups. The sums of slice s over adapter a go to slot s + a
-// of `slots`: in the order of the positions, each next pair has a larger s, a or both.
+// grid: token slices x input-block groups.
 template <int P, typename T, int NT, int TT, int NG, int RI, int RJ>
 __global__ void __launch_bounds__(NT, 1)
-k_circ_many_gc(const T* __restrict__ g, const T* __restrict__ x, float* __restrict__ slots, int q, int QJ,
+k_circ_many_gc(const T* __restrict__ g, const T* __restrict__ x, float* grad_c, float* slots, int q, int QJ,
                PlanView plan) {
   griddep_wait();
   if (!plan_matches(plan)) return;
   SliceWalk walk(plan);
   while (walk.next(plan)) {
-    circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, slots + ((int64_t)blockIdx.x + walk.ad) * q * q * P,
+    circ_gc_body<P, T, NT, TT, NG, RI, RJ>(g, x, walk.sums(grad_c, slots, (int64_t)q * q * P),
                                            PlannedPositions{plan.order}, walk.beg, walk.end, q, QJ, true, 0);
     __syncthreads();                                        // the segment's last tile is consumed
   }
@@ -192,7 +201,7 @@ static cudaError_t run_many_gc(const CircMany& a, int QJ, cudaStream_t s, GcSink
   const cudaError_t e = set_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)slices, (unsigned)njgroups), dim3(NT), smem, s,
-                    static_cast<const T*>(a.g), static_cast<const T*>(a.in), sink->partial, q, QJ,
+                    static_cast<const T*>(a.g), static_cast<const T*>(a.in), a.grad_c, sink->partial, q, QJ,
                     plan_view(a.plan, a.T, a.n, 0));
 }
 

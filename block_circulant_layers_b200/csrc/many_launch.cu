@@ -24,7 +24,7 @@ cudaError_t launch_circ_many(int op, const CircMany& a, int p, int dtype, cudaSt
 
 // grad_c[a] = the slots of adapter a added in slice order: with S <= T' slices of T' planned tokens,
 // slice s holds positions [T' s / S, T' (s + 1) / S), and its sums over adapter a lie in slot
-// s + a. Zeros for an adapter without tokens. kSplit threads share an element, each adding
+// s + a, or already in grad_c if the slice holds all of a. Zeros for an adapter without tokens. kSplit threads share an element, each adding
 // every kSplit-th slot, and their sums are added in order: the order depends on the plan alone.
 constexpr int kSumThreads = 256, kSplit = 8;
 
@@ -40,9 +40,11 @@ __global__ void __launch_bounds__(kSumThreads) k_sum_slots(const float4* __restr
   slices = (int)min((int64_t)slices, tokens);
   const int beg = __ldg(plan.offsets + ad), end = __ldg(plan.offsets + ad + 1);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // the slice of a position: the last s with tokens s / slices <= position
+  const int first = beg < end ? (int)(((int64_t)(beg + 1) * slices - 1) / tokens) : 0;
+  const int last = beg < end ? (int)(((int64_t)end * slices - 1) / tokens) : 0;
+  if (beg < end && first == last) return;
   if (e < n4 && beg < end) {
-    // the slice of a position: the last s with tokens s / slices <= position
-    const int first = (int)(((int64_t)(beg + 1) * slices - 1) / tokens), last = (int)(((int64_t)end * slices - 1) / tokens);
 #pragma unroll 4
     for (int s = first + r; s <= last; s += kSplit) {
       const float4 v = __ldcs(slots + (int64_t)(s + ad) * n4 + e);
