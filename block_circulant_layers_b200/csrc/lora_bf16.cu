@@ -660,8 +660,8 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
   };
   // sums of adapter ad to global memory; acc[8 i + 4 j + 2 h + e] is row rho0 + 16 i + g + 8 h,
   // column 16 wc + 8 j + 2 q + e
-  auto write = [&](int ad) {
-    const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
+  auto scale_of = [&](int ad) { return (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f; };
+  auto write = [&](int ad, float scale) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -775,7 +775,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
           for (int e = 0; e < NA; ++e) head[e * kThreads + tid] = acc[e];
           from_before = false;
         } else {
-          write(ad);
+          write(ad, scale_of(ad));
         }
         clear();
       }
@@ -794,14 +794,14 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
         if (__ldg(a.plan.tiles + klo).y != open) break;
         add_from(acc, head, k);
       }
-      write(open);
+      write(open, scale_of(open));
     }
     cluster_arrive();
   }
-  // adapters without tokens, shared by the cluster
+  // adapters without tokens, shared by the cluster: zeros, whatever their scale holds
   clear();
   for (int ad = rank; ad < a.plan.n; ad += C)
-    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
+    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad, 1.0f);
   if (C > 1) cluster_wait();                                   // the others are done with this CTA's memory
   if (early) griddep_wait();
 }

@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
       }
     }
   };
-  auto write = [&](int ad) {
-    const float scale = (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f;
+  auto scale_of = [&](int ad) { return (!is_a && a.scale) ? __ldg(a.scale + ad) : 1.0f; };
+  auto write = [&](int ad, float scale) {
 #pragma unroll
     for (int v = 0; v < NA / 4; ++v) {
       int rho, c;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
           for (int e = 0; e < NA; ++e) head[e * kThreads + tid] = sum[e];
           from_before = false;
         } else {
-          write(ad);
+          write(ad, scale_of(ad));
         }
       }
     }
@@ -515,14 +515,14 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
         if (__ldg(a.plan.tiles + klo).y != open) break;
         add_from(sum, head, k);
       }
-      write(open);
+      write(open, scale_of(open));
     }
     cluster_arrive();
   }
 #pragma unroll
   for (int e = 0; e < NA; ++e) sum[e] = 0.0f;
-  for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens
-    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad);
+  for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens: zeros, whatever their scale holds
+    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad, 1.0f);
   if (C > 1) cluster_wait();                                // the others are done with this CTA's memory
   if (early) griddep_wait();
 }

@@ -1,0 +1,47 @@
+"""Edges of the many-adapter operators: adapters that no token uses, values that are not finite,
+long sums, plans that do not fit, and what a call leaves behind."""
+import pytest
+import torch
+
+from many_util import make_ids
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def rd():
+    if not torch.cuda.is_available():
+        pytest.fail("a CUDA GPU is required for the gpu tests")
+    import block_circulant_layers_b200 as rd
+    return rd
+
+
+def randn(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).cuda()
+
+
+# ----------------------------------------------------------------- adapters without tokens
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,r", [(0, 16), (30, 8), (30, 64), (1200, 24), (1200, 128)])
+def test_an_idle_adapters_scale_is_not_used(rd, T, r, dtype):
+    """The gradients of an adapter without tokens are zeros even where its scale is not finite, and
+    the others' gradients have the same bits as with a finite one."""
+    n, K, N, dt = 6, 136, 200, DT[dtype]
+    ids = make_ids("mixed", T, 3, seed=2) * 2                 # adapters 0, 2 and 4, or -2: none
+    x, g = randn(1, T, K, dtype=dt), randn(2, T, N, dtype=dt)
+    a, b = randn(3, n, r, K, std=0.1, dtype=dt), randn(4, n, N, r, std=0.2, dtype=dt)
+    scale = 0.5 + torch.rand(n, generator=torch.Generator().manual_seed(5)).cuda()
+    plan = rd.adapter_plan(ids.cuda(), n)
+    u = torch.empty(T, r, device="cuda")
+    rd.lora_fwd(x, a, b, plan, scale=scale, u=u)
+    want = rd.lora_bwd(g, x, a, b, plan, u, scale=scale)
+    for k, bad in ((1, float("nan")), (3, float("inf")), (5, -float("inf"))):
+        scale[k] = bad
+    got = rd.lora_bwd(g, x, a, b, plan, u, scale=scale)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    for t in got[1:]:
+        assert not bool(t[1::2].any())
