@@ -41,6 +41,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The additions inside mma truncate: a sum left in its accumulator loses up to a step (2^-23) at
+// each of them, always towards zero (262144 tokens of one adapter: gradients 2e-4 too small). So an
+// accumulator takes the products of one step of a loop only (4 to 12 mma), and the steps' sums
+// are added by FADD, rounded to nearest.
+__device__ __forceinline__ void add4(float (&acc)[4], const float (&d)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] += d[e];
+}
+
 __device__ __forceinline__ uint4 ldg16(const bf16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 // N consecutive 32-bit words (N = 1, 2, 4, 8) through the read-only path.
@@ -135,66 +144,72 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) k_lora_rows16(LoraR
     const bf16_t* const row0 = a.in + (int64_t)tok[0] * K;
     const bf16_t* const row1 = a.in + (int64_t)tok[1] * K;
     const bf16_t* const w1 = a.w1 + (int64_t)ad * r * K;
-    float acc[NJ][4];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-
+    // in runs of kRun units (2 kRun mma), each run's sums added to this warp's in shared memory
+    constexpr int kRun = 4;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-    for (int u = u0 + warp; u < u1; u += WK) {
-      const int k0 = 32 * u + 8 * q;                           // this lane's 8 columns
-      const bool in = k0 < K;
-      const uint4 x0 = (in && tok[0] >= 0) ? ldg16(row0 + k0) : zero;
-      const uint4 x1 = (in && tok[1] >= 0) ? ldg16(row1 + k0) : zero;
-      if constexpr (!BWD) {
-        // w1 row 8 j + g, the same 8 columns
+    int u = u0 + warp;
+    for (bool first = true; first || u < u1; first = false) {
+      float acc[NJ][4];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int rho = 8 * j + g;
-          const uint4 wb = (in && rho < r) ? ldg16(w1 + (int64_t)rho * K + k0) : zero;
-          mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, wb.x, wb.y);
-          mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, wb.z, wb.w);
-        }
-      } else {
-        // w1 is read where B lies: column k0 + e of w1 is row k0 + e of B, r values of which
-        // this lane takes V, so tile j holds the r index V g + j at its column g
-        uint32_t wr[8][V / 2];
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+      const int end = min(u1, u + kRun * WK);
+#pragma unroll (R <= 32 ? 2 : 1)
+      for (; u < end; u += WK) {
+        const int k0 = 32 * u + 8 * q;                         // this lane's 8 columns
+        const bool in = k0 < K;
+        const uint4 x0 = (in && tok[0] >= 0) ? ldg16(row0 + k0) : zero;
+        const uint4 x1 = (in && tok[1] >= 0) ? ldg16(row1 + k0) : zero;
+        if constexpr (!BWD) {
+          // w1 row 8 j + g, the same 8 columns
 #pragma unroll
-          for (int x = 0; x < V / 2; ++x) wr[e][x] = 0;
-          if (in) {
-            if constexpr (V <= 8) {
-              if (V * g < r) ldg_words<V / 2>(w1 + (int64_t)(k0 + e) * r + V * g, wr[e]);
-            } else {
+          for (int j = 0; j < NJ; ++j) {
+            const int rho = 8 * j + g;
+            const uint4 wb = (in && rho < r) ? ldg16(w1 + (int64_t)rho * K + k0) : zero;
+            mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, wb.x, wb.y);
+            mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, wb.z, wb.w);
+          }
+        } else {
+          // w1 is read where B lies: column k0 + e of w1 is row k0 + e of B, r values of which
+          // this lane takes V, so tile j holds the r index V g + j at its column g
+          uint32_t wr[8][V / 2];
 #pragma unroll
-              for (int hv = 0; hv < 2; ++hv) {
-                uint32_t t[4] = {0, 0, 0, 0};
-                if (V * g + 8 * hv < r) ldg_words<4>(w1 + (int64_t)(k0 + e) * r + V * g + 8 * hv, t);
+          for (int e = 0; e < 8; ++e) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) wr[e][4 * hv + x] = t[x];
+            for (int x = 0; x < V / 2; ++x) wr[e][x] = 0;
+            if (in) {
+              if constexpr (V <= 8) {
+                if (V * g < r) ldg_words<V / 2>(w1 + (int64_t)(k0 + e) * r + V * g, wr[e]);
+              } else {
+#pragma unroll
+                for (int hv = 0; hv < 2; ++hv) {
+                  uint32_t t[4] = {0, 0, 0, 0};
+                  if (V * g + 8 * hv < r) ldg_words<4>(w1 + (int64_t)(k0 + e) * r + V * g + 8 * hv, t);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) wr[e][4 * hv + x] = t[x];
+                }
               }
             }
           }
-        }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, pair_of(wr[0], wr[1], j), pair_of(wr[2], wr[3], j));
-          mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, pair_of(wr[4], wr[5], j), pair_of(wr[6], wr[7], j));
+          for (int j = 0; j < NJ; ++j) {
+            mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, pair_of(wr[0], wr[1], j), pair_of(wr[2], wr[3], j));
+            mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, pair_of(wr[4], wr[5], j), pair_of(wr[6], wr[7], j));
+          }
         }
       }
+      // the column of tile j that a lane holds is 2 q + e
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = g + 8 * (e / 2), c = 2 * q + (e & 1);
+          float& sum = part[(warp * M + t) * R + (BWD ? V * c + j : 8 * j + c)];
+          sum = first ? acc[j][e] : sum + acc[j][e];
+        }
     }
     if (gr0 < g1) load_base(gr0);
-    // the column of tile j that a lane holds is 2 q + e
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = g + 8 * (e / 2), c = 2 * q + (e & 1);
-        part[(warp * M + t) * R + (BWD ? V * c + j : 8 * j + c)] = acc[j][e];
-      }
     __syncthreads();
     // this CTA's sum, in place of the first share
     for (int e = 4 * threadIdx.x; e < M * R; e += 4 * kThreads) {
@@ -476,18 +491,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
       request();
       const uint32_t x_at = ring_at + slot * S::kStage, w_at = x_at + S::kRowBytes;
       slot = slot + 1 == S::kStages ? 0 : slot + 1;
+      uint32_t x[COLS / 32][4];
 #pragma unroll
-      for (int k = COLS / 2 * wh; k < COLS / 2 * (wh + 1); k += 16) {
-        uint32_t x[4];
-        ldsm4(x, x_at + moved<COLS>(x_off, 0, k));
+      for (int s = 0; s < COLS / 32; ++s) ldsm4(x[s], x_at + moved<COLS>(x_off, 0, COLS / 2 * wh + 16 * s));
 #pragma unroll
-        for (int j = 0; j < R / 16; ++j) {
+      for (int j = 0; j < R / 16; ++j) {
+        float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // this step's sums
+#pragma unroll
+        for (int s = 0; s < COLS / 32; ++s) {
+          const int k = COLS / 2 * wh + 16 * s;
           uint32_t w[4];
           if constexpr (!BWD) ldsm4(w, w_at + moved<COLS>(w1_off, 16 * j, k));
           else ldsm4t(w, w_at + moved<R>(w1_off, k, 16 * j));
-          mma16816(acc[2 * j], x[0], x[1], x[2], x[3], w[0], w[1]);
-          mma16816(acc[2 * j + 1], x[0], x[1], x[2], x[3], w[2], w[3]);
+          mma16816(d0, x[s][0], x[s][1], x[s][2], x[s][3], w[0], w[1]);
+          mma16816(d1, x[s][0], x[s][1], x[s][2], x[s][3], w[2], w[3]);
         }
+        add4(acc[2 * j], d0);
+        add4(acc[2 * j + 1], d1);
       }
     }
 #pragma unroll
@@ -748,24 +768,30 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
       __syncthreads();
       const uint32_t x_at = ring_at + i % S::kStages * S::kStage;
       const int tokens = desc[i + 2].x - desc[i + 1].x, ad = desc[i + 1].y;
+      float d[NI][2][4];                                       // this tile's sums
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[j][e / 4][e % 4] = 0.0f;
 #pragma unroll
       for (int k = 0; k < S::kTok; k += 16) {
         if (k >= tokens) break;
         uint32_t b[4];
         ldsm4t(b, x_at + moved<COLS>(x_off, k, 0));
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          float(&d0)[4] = *reinterpret_cast<float(*)[4]>(acc + 8 * j);
-          float(&d1)[4] = *reinterpret_cast<float(*)[4]>(acc + 8 * j + 4);
+        for (int j = 0; j < NI; ++j)
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             uint32_t f[4];
             ldsm4t(f, mid_at + s * S::kTok * R * 2 + moved<R>(m_off, k, 16 * j));
-            mma16816(d0, f[0], f[1], f[2], f[3], b[0], b[1]);
-            mma16816(d1, f[0], f[1], f[2], f[3], b[2], b[3]);
+            mma16816(d[j][0], f[0], f[1], f[2], f[3], b[0], b[1]);
+            mma16816(d[j][1], f[0], f[1], f[2], f[3], b[2], b[3]);
           }
-        }
       }
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[8 * j + e] += d[j][e / 4][e % 4];
       const bool goes_on = desc[i + 2].y == ad;                // the next tile is the same adapter's
       if (w0 + i + 1 == share.hi && goes_on && !from_before) {
         open = ad;                                             // its sums stay here

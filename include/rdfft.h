@@ -320,8 +320,10 @@ int adapter_plan(const int32_t* ids, int64_t T, int n, int32_t* plan, rdfft_stre
  *   plan  : the plan of the batch (same T and n).
  *   K, N  : multiples of 8 in [8, 65536].   r : a multiple of 8 in [8, 128] (a smaller rank is
  *           padded with zero rows of A and zero columns of B, which changes no result).
- * Sums are fp32. In bf16, u enters the second product as the sum of two bf16 (16 mantissa bits)
- * and y is rounded once. The result is the same on every run. An infinity or NaN stays within
+ * Sums are fp32. In bf16, up to 12 tensor-core products of 16 terms are added inside the tensor
+ * core, whose additions truncate (each short by 2^-23 of the sum at most); those sums are then added
+ * rounded to nearest, so long sums do not shrink. u enters the second product as the sum of two
+ * bf16 (16 mantissa bits) and y is rounded once. The result is the same on every run. An infinity or NaN stays within
  * its token (or, in a weight, its adapter), where a bf16 result may be NaN instead of infinite.
  */
 int lora_fwd(const void* x, const void* a, const void* b, const float* scale, const void* base, void* y, float* u,
@@ -338,8 +340,9 @@ int lora_fwd(const void* x, const void* a, const void* b, const float* scale, co
  *   v      : T x r fp32 workspace of the caller, needed with grad_a (else it may be NULL);
  *            left holding v. Calls that share it must be ordered on one stream.
  * What a skipped gradient alone needs may be NULL: x for grad_a, u for grad_b, a for grad_x.
- * No output may overlap any other argument. Sums over tokens run in a fixed order: the
- * gradients are the same on every run.
+ * No output may overlap any other argument. Sums over tokens are fp32 as in lora_fwd and run in a
+ * fixed order: the gradients are the same on every run. v is rounded to fp32 before grad_a's sum
+ * (in bf16, u and v enter it as three bf16 each, 24 mantissa bits).
  */
 int lora_bwd(const void* g, const void* x, const void* a, const void* b, const float* scale, const float* u, float* v,
              void* grad_x, float* grad_a, float* grad_b, const int32_t* plan, int64_t T, int K, int N, int r, int n,

@@ -45,3 +45,32 @@ def test_an_idle_adapters_scale_is_not_used(rd, T, r, dtype):
         assert torch.equal(p, q)
     for t in got[1:]:
         assert not bool(t[1::2].any())
+
+
+# ------------------------------------------------------------------------------ long sums
+def shrink(got, ref):
+    """Mean over all elements of how far the result falls short, relative (its terms all positive)."""
+    return float(((ref - got.double()) / ref).mean())
+
+
+@pytest.mark.parametrize("T,K,r", [(16, 65536, 16), (40, 65536, 128), (2048, 65536, 16), (1100, 65536, 128),
+                                   (262144, 256, 16), (65536, 256, 64), (32768, 256, 128)])
+def test_long_bf16_sums_do_not_shrink(rd, T, K, r):
+    """u, grad_a and grad_b (fp32) of positive bf16 operands in 64 bits. Roundings to nearest have mean
+    zero; truncating ones would make every sum smaller, in proportion to its length. A tensor-core
+    accumulator takes at most 12 additions (three products of 64 tokens), 8 for u and v, each short by
+    at most a step, 2 U; 4 U for what the roundings to nearest leave in the mean."""
+    U, n, N = 2.0 ** -24, 1, 64 if K > 1024 else 256
+    x, g = randn(1, T, K).abs().bfloat16(), randn(2, T, N).abs().bfloat16()
+    a, b = (randn(3, n, r, K).abs() * K ** -0.5).bfloat16(), (randn(4, n, N, r).abs() * r ** -0.5).bfloat16()
+    plan = rd.adapter_plan(torch.zeros(T, dtype=torch.int32, device="cuda"), n)
+    u = torch.empty(T, r, device="cuda")
+    rd.lora_fwd(x, a, b, plan, u=u)
+    _, ga, gb = rd.lora_bwd(g, x, a, b, plan, u)
+    v = g.double() @ b[0].double()
+    ref_u = torch.cat([t.double() @ a[0].double().t() for t in x.split(1 << 13)])
+    ref_ga = sum(p.t() @ t.double() for p, t in zip(v.split(1 << 13), x.split(1 << 13)))
+    ref_gb = g.double().t() @ u.double()
+    assert abs(shrink(u, ref_u)) <= (8 * 2 + 4) * U
+    assert abs(shrink(gb[0], ref_gb)) <= (12 * 2 + 4) * U
+    assert abs(shrink(ga[0], ref_ga)) <= (12 * 2 + 8 * 2 + 4) * U          # v is such a sum as well
