@@ -94,7 +94,8 @@ def block_circulant_many(x: torch.Tensor, c: torch.Tensor, p: int, plan: _b.Adap
 
 
 class LowRankAdapters(torch.nn.Module):
-    """n low-rank adapters in_features -> out_features of rank r, scaled by alpha / r.
+    """n low-rank adapters in_features -> out_features of rank r, scaled by alpha / r (the buffer
+    `scale`, one value per adapter, fp32 whatever dtype the module is converted to).
 
     a is initialised i.i.d. N(0, 1/in_features), b to zero (each adapter starts as no change).
     r is a multiple of 8 up to 128."""
@@ -109,6 +110,15 @@ class LowRankAdapters(torch.nn.Module):
         self.b = torch.nn.Parameter(torch.zeros(n, out_features, r, device=device, dtype=torch.float32))
         self.register_buffer("scale", torch.full((n,), (r if alpha is None else alpha) / r, dtype=torch.float32,
                                                  device=device))
+
+    def _apply(self, fn, recurse=True):
+        # .to(dtype) and the like move the scale with the parameters but leave it fp32: rounded to
+        # bf16 it would change every output by up to 2^-9
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
 
     def forward(self, x: torch.Tensor, plan: _b.AdapterPlan, base: torch.Tensor | None = None) -> torch.Tensor:
         return low_rank_many(x, self.a, self.b, plan, self.scale.float(), base)

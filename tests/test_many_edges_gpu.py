@@ -74,3 +74,24 @@ def test_long_bf16_sums_do_not_shrink(rd, T, K, r):
     assert abs(shrink(u, ref_u)) <= (8 * 2 + 4) * U
     assert abs(shrink(gb[0], ref_gb)) <= (12 * 2 + 4) * U
     assert abs(shrink(ga[0], ref_ga)) <= (12 * 2 + 8 * 2 + 4) * U          # v is such a sum as well
+
+
+# -------------------------------------------------------------------- a module's own dtype
+def test_a_converted_bank_keeps_its_scale(rd):
+    """alpha / r = 8 / 24 in a bank converted to bf16, with fp32 activations and weights that make
+    y = scale x_0: two roundings of half a step (2^-24), of the scale and of the product."""
+    n, K, r, T = 1, 64, 24, 40
+    bank = rd.LowRankAdapters(n, K, 8, r, alpha=8.0, device="cuda").to(torch.bfloat16)
+    with torch.no_grad():
+        bank.a.zero_()
+        bank.a[0, 0, 0] = 1.0                                 # u = (x_0, 0, ...)
+        bank.b[0, :, 0] = 1.0                                 # y = scale x_0 in every column
+    x = torch.arange(1, T + 1, device="cuda", dtype=torch.float32)[:, None].repeat(1, K)
+    plan = rd.adapter_plan(torch.zeros(T, dtype=torch.int32, device="cuda"), n)
+    y = bank(x, plan)                                         # fp32 activations, bf16 weights
+    want = x[:, :8].double() * (8.0 / 24.0)
+    assert float(((y.detach().double() - want) / want).abs().max()) <= 2 * 2.0 ** -24
+    y.sum().backward()
+    assert bank.b.grad.dtype == torch.bfloat16
+    want_b = float(x[:, 0].double().sum()) * (8.0 / 24.0)     # each column's sum of scale u, rounded to bf16
+    assert float((bank.b.grad[0, :, 0].double() - want_b).abs().max()) <= (2.0 ** -8 + 1e-6) * want_b
