@@ -91,7 +91,8 @@ struct LoraWgrad {
 
 // The part for grad_b reads nothing that the rows kernel writes, so its CTAs need not wait for
 // it: the rows kernel lets them start only after all work before it has completed. They wait
-// before they exit, so that the grid still ends after the rows kernel.
+// before they exit, on every path, so that the grid still ends after the rows kernel (a launch
+// behind it might otherwise write the plan or v while the rows kernel reads them).
 __device__ __forceinline__ bool starts_early(bool after_rows, bool is_a) { return after_rows && !is_a; }
 
 // The weight gradients share the batch evenly: CTA `rank` of a cluster of C takes an equal part

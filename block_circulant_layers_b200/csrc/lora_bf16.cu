@@ -662,7 +662,10 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
   const bool is_a = block >= blocks_b;                         // grad_b's blocks first: they start early
   const bool early = starts_early(a.after_rows, is_a);
   if (!early) griddep_wait();
-  if (!plan_matches(a.plan)) return;
+  if (!plan_matches(a.plan)) {
+    if (early) griddep_wait();
+    return;
+  }
   const int n0 = S::kCols * (is_a ? block - blocks_b : block);
   const int W = is_a ? a.K : a.N;                              // columns of the rows read
   const bf16_t* const rows = is_a ? a.x : a.g;

@@ -343,7 +343,10 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
   const bool is_a = block >= blocks_b;                         // grad_b's blocks first: they start early
   const bool early = starts_early(a.after_rows, is_a);
   if (!early) griddep_wait();
-  if (!plan_matches(a.plan)) return;
+  if (!plan_matches(a.plan)) {
+    if (early) griddep_wait();
+    return;
+  }
   const int n0 = 64 * (is_a ? block - blocks_b : block);
   const int W = is_a ? a.K : a.N;
   const float* const rows = is_a ? a.x : a.g;

@@ -563,7 +563,7 @@ const char* rdfft_strerror(int code) {
       return "the workspace is smaller than circ_bwd_workspace_size (circ_bwd_many_workspace_size, "
              "grad_norm_workspace_size) reports for this call (for circ_bwd_deterministic_noalloc: the call needs "
              "more than its built-in 16 MiB of scratch)";
-    case RDFFT_EPLAN: return "a kernel was given an adapter plan made for other sizes; its outputs were not written";
+    case RDFFT_EPLAN: return "a kernel was given an adapter plan made for other sizes; its outputs are not valid";
     case RDFFT_ECUDA:
       snprintf(t_msg, sizeof(t_msg), "CUDA error while enqueuing: %s (%d)", cudaGetErrorString(t_last_cuda),
                (int)t_last_cuda);

@@ -303,8 +303,9 @@ int adapter_plan_size(int64_t T, int n, int64_t* words);
  * from 16 + (n + 2 rounded up to 4), T words of token order. Positions offsets[a] up to
  * offsets[a + 1] of the order are the tokens of adapter a, ascending; a = n is the group
  * without an adapter. The same on every run.
- * A call that is given a plan of another T or n leaves its outputs unwritten, and
- * rdfft_take_device_error then returns RDFFT_EPLAN.
+ * A call that is given a plan of another T or n leaves its outputs unwritten (but for grad_c of
+ * circ_bwd_many, whose contents are then undefined), and rdfft_take_device_error then returns
+ * RDFFT_EPLAN.
  */
 int adapter_plan(const int32_t* ids, int64_t T, int n, int32_t* plan, rdfft_stream_t stream);
 

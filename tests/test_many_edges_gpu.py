@@ -95,3 +95,36 @@ def test_a_converted_bank_keeps_its_scale(rd):
     assert bank.b.grad.dtype == torch.bfloat16
     want_b = float(x[:, 0].double().sum()) * (8.0 / 24.0)     # each column's sum of scale u, rounded to bf16
     assert float((bank.b.grad[0, :, 0].double() - want_b).abs().max()) <= (2.0 ** -8 + 1e-6) * want_b
+
+
+# ------------------------------------------------------------------- plans that do not fit
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("wants", [(1, 0, 1), (1, 1, 1), (0, 1, 0), (0, 0, 1)])
+def test_backward_with_a_plan_of_other_sizes(rd, wants, dtype):
+    """Through the C ABI (the binding refuses it earlier), the plan made again right behind it and
+    used: nothing is written by the first call, the device error says so, the second is right."""
+    T, n, K, N, r, dt = 90, 2, 64, 72, 8, (torch.float32, torch.bfloat16)[dtype]
+    ids = make_ids("mixed", T, n, seed=1).cuda()
+    x, g, a, b = (randn(k, *s, dtype=dt) for k, s in ((1, (T, K)), (2, (T, N)), (3, (n, r, K)), (4, (n, N, r))))
+    good = rd.adapter_plan(ids, n)
+    u = torch.empty(T, r, device="cuda")
+    rd.lora_fwd(x, a, b, good, u=u)
+    want = rd.lora_bwd(g, x, a, b, good, u)
+    buf = rd.adapter_plan(torch.zeros(4 * T, dtype=torch.int32, device="cuda"), n).buf     # larger: reads stay inside
+    outs = [torch.full_like(t, 7.0) if w else None for t, w in zip(want, wants)]
+    v = torch.full((T, r), 7.0, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert rd.take_device_error() == 0
+
+    def call():
+        p = [None if t is None else t.data_ptr() for t in outs]
+        assert rd.lib.lora_bwd(g.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), None, u.data_ptr(),
+                               v.data_ptr(), *p, buf.data_ptr(), T, K, N, r, n, dtype, s) == 0
+
+    call()
+    kept = [None if t is None else t.clone() for t in [*outs, v]]
+    assert rd.lib.adapter_plan(ids.data_ptr(), T, n, buf.data_ptr(), s) == 0
+    call()
+    assert rd.take_device_error() == rd.RDFFT_EPLAN and rd.take_device_error() == 0
+    assert all(t is None or bool((t == 7.0).all()) for t in kept)
+    assert all(t is None or torch.equal(t, w) for t, w in zip(outs, want))
