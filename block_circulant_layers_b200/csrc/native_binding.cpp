@@ -70,6 +70,16 @@ float* fptr(const MaybeTensor& t) { return static_cast<float*>(ptr(t)); }
 py::object maybe(const MaybeTensor& t) { return t ? py::cast(*t) : py::object(py::none()); }
 
 // ------------------------------------------------------------------------------- plan
+// The buffer of a plan of T tokens and n adapters: the kernels index it by those sizes.
+void plan_buffer(const Tensor& buf, int64_t T, int n, const Tensor& ref) {
+  int64_t words = 0;
+  const bool sizes = adapter_plan_size(T, n, &words) == RDFFT_OK;
+  if (!sizes || !buf.is_cuda() || !buf.is_contiguous() || buf.scalar_type() != at::kInt || buf.numel() < words ||
+      buf.device() != ref.device())
+    throw py::value_error("the plan's buffer must be adapter_plan's int32 tensor for its " + std::to_string(T) +
+                          " tokens and " + std::to_string(n) + " adapters, on " + ref.device().str());
+}
+
 py::tuple adapter_plan_(const Tensor& ids, int n, const MaybeTensor& buf) {
   dense(ids, "ids");
   if (ids.scalar_type() != at::kInt || ids.dim() != 1)
@@ -78,6 +88,7 @@ py::tuple adapter_plan_(const Tensor& ids, int n, const MaybeTensor& buf) {
   int64_t words = 0;
   const int rc = adapter_plan_size(T, n, &words);
   if (rc != RDFFT_OK) return py::make_tuple(rc, py::none());
+  if (buf) plan_buffer(*buf, T, n, ids);
   const c10::cuda::OptionalCUDAGuard guard(ids.device());
   Tensor plan = buf ? *buf : at::empty({words}, ids.options());
   const int code = adapter_plan(ids.const_data_ptr<int>(), T, n, plan.mutable_data_ptr<int>(), stream_of(ids));
@@ -94,6 +105,7 @@ void plan_for(const Tensor& plan, int64_t T, int n, const Tensor& rows, int64_t 
   if (T != (width ? rows.numel() / width : 0) || n != adapters || plan.device() != rows.device())
     throw py::value_error("the plan is for " + std::to_string(T) + " tokens and " + std::to_string(n) +
                           " adapters on " + plan.device().str() + ", not for " + of);
+  plan_buffer(plan, T, n, rows);
 }
 
 // --------------------------------------------------------------------------- low rank

@@ -128,3 +128,20 @@ def test_backward_with_a_plan_of_other_sizes(rd, wants, dtype):
     assert rd.take_device_error() == rd.RDFFT_EPLAN and rd.take_device_error() == 0
     assert all(t is None or bool((t == 7.0).all()) for t in kept)
     assert all(t is None or torch.equal(t, w) for t, w in zip(outs, want))
+
+
+def test_a_plan_whose_buffer_does_not_hold_it_is_refused(rd):
+    T, n, K = 200, 3, 64
+    ids = make_ids("mixed", T, n).cuda()
+    plan = rd.adapter_plan(ids, n)
+    x, a, b, c_hat = randn(1, T, K), randn(2, n, 8, K), randn(3, n, K, 8), randn(4, n, 1, 1, K)
+    u = torch.zeros(T, 8, device="cuda")
+    for buf in (plan.buf[:-4], plan.buf[:0], plan.buf.float(), plan.buf.cpu(), torch.stack([plan.buf] * 2, 1)[:, 0]):
+        bad = rd.AdapterPlan(T, n, buf)
+        for call in (lambda: rd.adapter_plan(ids, n, out=bad), lambda: rd.lora_fwd(x, a, b, bad),
+                     lambda: rd.lora_bwd(x, x, a, b, bad, u), lambda: rd.circ_fwd_many(x, c_hat, K, bad),
+                     lambda: rd.circ_bwd_many(x, x, c_hat, K, bad)):
+            with pytest.raises(ValueError):
+                call()
+    rd.lora_fwd(x, a, b, plan)
+    assert rd.take_device_error() == 0
