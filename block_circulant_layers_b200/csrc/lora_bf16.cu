@@ -450,14 +450,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
       if (rstep < n1 || a.base != nullptr) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          if (tok[h] >= 0) cp16(x_dst + slot + h * ROWS * COLS * 2, px[h], rcol < RW);
+          if (tok[h] >= 0) cp16(x_dst + slot + h * ROWS * COLS * 2, rcol < RW ? px[h] : a.in, rcol < RW);
           px[h] += COLS * C;
         }
       }
       if (adapted) {
 #pragma unroll
         for (int i = 0; i < WL; ++i) {
-          if (UNITS * R >= kThreads || tid < UNITS * R) cp16(w_dst[i] + slot, pw[i], w_in[i] && wcol[i] < RW);
+          const bool in = w_in[i] && wcol[i] < RW;
+          if (UNITS * R >= kThreads || tid < UNITS * R) cp16(w_dst[i] + slot, in ? pw[i] : a.w1, in);
           pw[i] += w_go;
           wcol[i] += COLS * C;
         }
