@@ -335,7 +335,6 @@ def adapter_plan(ids: torch.Tensor, n: int, out: AdapterPlan | None = None) -> A
         return AdapterPlan(ids.numel(), n, buf)
     if out.T != ids.numel() or out.n != n or out.buf.device != ids.device:
         raise ValueError("out must be a plan of the same number of tokens and adapters on the same device")
-    torch.autograd.graph.increment_version(out.buf)          # a backward pass that saved it must not use it now
     _check(_native.adapter_plan(ids, n, out.buf)[0], "adapter_plan")
     return out
 

@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 #include <vector>
@@ -67,6 +68,16 @@ void* ptr(const Tensor& t) { return t.data_ptr(); }
 void* ptr(const MaybeTensor& t) { return t ? t->data_ptr() : nullptr; }
 float* fptr(const MaybeTensor& t) { return static_cast<float*>(ptr(t)); }
 
+// The call behind `code` wrote into tensors that the caller gave: a graph that saved one of them must
+// not go on with the new values unnoticed. (An inference tensor counts no versions.)
+void written(int code, const Tensor& t) {
+  if (code == RDFFT_OK && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(int code, std::initializer_list<const MaybeTensor*> given) {
+  for (const MaybeTensor* t : given)
+    if (*t) written(code, **t);
+}
+
 py::object maybe(const MaybeTensor& t) { return t ? py::cast(*t) : py::object(py::none()); }
 
 // ------------------------------------------------------------------------------- plan
@@ -92,6 +103,7 @@ py::tuple adapter_plan_(const Tensor& ids, int n, const MaybeTensor& buf) {
   const c10::cuda::OptionalCUDAGuard guard(ids.device());
   Tensor plan = buf ? *buf : at::empty({words}, ids.options());
   const int code = adapter_plan(ids.const_data_ptr<int>(), T, n, plan.mutable_data_ptr<int>(), stream_of(ids));
+  written(code, {&buf});
   return py::make_tuple(code, plan);
 }
 
@@ -142,6 +154,7 @@ py::tuple lora_fwd_(const Tensor& x, const Tensor& a, const Tensor& b, const Ten
   Tensor y = out_of(y_, "y", s.out, x.scalar_type(), x);
   const int code = lora_fwd(ptr(x), ptr(a), ptr(b), fptr(scale), ptr(base), ptr(y), fptr(u),
                             plan.const_data_ptr<int>(), T, s.K, s.N, s.r, n, dtype_code(x), stream_of(x));
+  written(code, {&y_, &u});
   return py::make_tuple(code, y);
 }
 
@@ -162,6 +175,10 @@ py::tuple lora_bwd_(const Tensor& g, const Tensor& x, const Tensor& a, const Ten
   like(v, "workspace", {T, s.r}, at::kFloat, x);
   const int code = lora_bwd(ptr(g), ptr(x), ptr(a), ptr(b), fptr(scale), fptr(u), fptr(v), ptr(gx), fptr(ga), fptr(gb),
                             plan.const_data_ptr<int>(), T, s.K, s.N, s.r, n, dtype_code(x), stream_of(x));
+  if (need_x) written(code, {&grad_x_});
+  if (need_a) written(code, {&grad_a_});
+  if (need_b) written(code, {&grad_b_});
+  if (need_x || need_a) written(code, {&workspace});
   return py::make_tuple(code, maybe(gx), maybe(ga), maybe(gb));
 }
 
@@ -186,6 +203,7 @@ py::tuple circ_fwd_many_(const Tensor& x, const Tensor& c_hat, int p, const Tens
   Tensor y = out_of(y_, "y", x.sizes(), x.scalar_type(), x);
   const int code = circ_fwd_many(ptr(x), c_hat.const_data_ptr<float>(), ptr(base), ptr(y), plan.const_data_ptr<int>(),
                                  T, D, p, n, code_of_type, stream_of(x));
+  written(code, {&y_});
   return py::make_tuple(code, y);
 }
 
@@ -212,6 +230,8 @@ py::tuple circ_bwd_many_(const Tensor& g, const Tensor& x, const Tensor& c_hat, 
   const int code = circ_bwd_many(ptr(g), ptr(x), c_hat.const_data_ptr<float>(), ptr(gx), fptr(gc),
                                  plan.const_data_ptr<int>(), T, D, p, n, type, ptr(ws), ws ? ws->nbytes() : 0,
                                  stream_of(x));
+  if (need_x) written(code, {&grad_x_});
+  if (need_c) written(code, {&grad_c_, &workspace_});
   return py::make_tuple(code, maybe(gx), maybe(gc));
 }
 
@@ -267,6 +287,8 @@ py::tuple norm_(const py::list& ts, bool clip, double max_norm, const std::optio
       clip ? clip_grad_norm(grads, out ? o.ptrs.data() : in.ptrs.data(), in.numels.data(), in.codes.data(), count,
                             (float)max_norm, n, buf.data_ptr(), need, stream_of(buf))
            : grad_norm(grads, in.numels.data(), in.codes.data(), count, n, buf.data_ptr(), need, stream_of(buf));
+  if (clip)
+    for (py::handle t : out ? *out : ts) written(code, THPVariable_Unpack(t.ptr()));
   return py::make_tuple(code, norm);
 }
 

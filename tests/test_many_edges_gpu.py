@@ -145,3 +145,60 @@ def test_a_plan_whose_buffer_does_not_hold_it_is_refused(rd):
                 call()
     rd.lora_fwd(x, a, b, plan)
     assert rd.take_device_error() == 0
+
+
+# ------------------------------------------------------------------- what a call leaves behind
+def test_a_graph_notices_what_a_call_overwrites(rd):
+    """Tensors that a call writes into count as modified in place, and no others do; a backward pass that
+    saved one fails instead of using the new values. Tensors made in inference mode are written too."""
+    T, n, K, r = 30, 2, 64, 8
+    plan = rd.adapter_plan(make_ids("mixed", T, n).cuda(), n)
+    x, a, b, g = randn(1, T, K), randn(2, n, r, K), randn(3, n, K, r), randn(4, T, K)
+    c_hat = randn(5, n, 1, 1, K)
+    new = {k: torch.empty(s, device="cuda") for k, s in dict(
+        y=(T, K), u=(T, r), gx=(T, K), ga=(n, r, K), gb=(n, K, r), ws=(T, r), gc=(n, 1, 1, K), out=(T, K)).items()}
+    import ctypes
+    need = ctypes.c_size_t()
+    rd.lib.circ_bwd_many_workspace_size(T, K, K, n, 0, 1, ctypes.byref(need))
+    new["cws"] = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    inputs = [x, a, b, g, c_hat]
+    seen = {k: t._version for k, t in new.items()}
+
+    def advanced():
+        k = {k for k, t in new.items() if t._version != seen[k]}
+        seen.update((k, t._version) for k, t in new.items())
+        return k
+
+    rd.lora_fwd(x, a, b, plan, y=new["y"], u=new["u"])
+    assert advanced() == {"y", "u"}
+    kw = dict(grad_x=new["gx"], grad_a=new["ga"], grad_b=new["gb"], workspace=new["ws"])
+    rd.lora_bwd(g, x, a, b, plan, new["u"], **kw)
+    assert advanced() == {"gx", "ga", "gb", "ws"}
+    rd.lora_bwd(g, x, a, b, plan, new["u"], need_grad_x=False, need_grad_a=False, **kw)
+    assert advanced() == {"gb"}
+    rd.circ_fwd_many(x, c_hat, K, plan, y=new["y"])
+    assert advanced() == {"y"}
+    rd.circ_bwd_many(g, x, c_hat, K, plan, grad_x=new["gx"], grad_c=new["gc"], workspace=new["cws"])
+    assert advanced() == {"gx", "gc", "cws"}
+    rd.grad_norm([x, new["gx"]])
+    rd.clip_grad_norm([x], 1.0, out=[new["out"]])
+    assert advanced() == {"out"}
+    rd.clip_grad_norm([new["gx"], new["ga"]], 1.0)
+    assert advanced() == {"gx", "ga"}
+    with pytest.raises(rd.RdfftError):
+        rd.clip_grad_norm([new["gx"]], -1.0)                  # refused: nothing written
+    assert advanced() == set() and all(t._version == 0 for t in inputs)
+
+    leaf = x.clone().requires_grad_(True)
+    h = leaf * 2.0
+    loss = h.square().sum()                                   # saves h
+    rd.circ_fwd_many(x, c_hat, K, plan, base=h.detach(), y=h.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        held = torch.zeros(T, K, device="cuda")
+        kept = rd.adapter_plan(make_ids("one", T, n).cuda(), n)
+    rd.circ_fwd_many(x, c_hat, K, plan, y=held)
+    rd.clip_grad_norm([held], 1.0)
+    assert bool(held.any())
+    assert rd.adapter_plan(make_ids("none", T, n).cuda(), n, out=kept).offsets.tolist() == [0, 0, 0, T]
