@@ -277,11 +277,10 @@ py::tuple norm_(const py::list& ts, bool clip, double max_norm, const std::optio
   const int rc = grad_norm_workspace_size(count, &need);
   if (rc != RDFFT_OK) return py::make_tuple(rc, py::none());
   const c10::cuda::OptionalCUDAGuard guard(in.first.device());
-  // the norm stands behind the workspace
-  const int64_t words = (int64_t)(need / sizeof(float));
-  Tensor buf = at::empty({words + 1}, in.first.options().dtype(at::kFloat));
-  Tensor norm = buf.select(0, words);
-  float* const n = buf.mutable_data_ptr<float>() + words;
+  // memory of its own for the norm: a caller may keep it long after the workspace
+  const Tensor buf = at::empty({(int64_t)need}, in.first.options().dtype(at::kByte));
+  const Tensor norm = at::empty({}, in.first.options().dtype(at::kFloat));
+  float* const n = norm.mutable_data_ptr<float>();
   const void* const* grads = const_cast<const void* const*>(in.ptrs.data());
   const int code =
       clip ? clip_grad_norm(grads, out ? o.ptrs.data() : in.ptrs.data(), in.numels.data(), in.codes.data(), count,

@@ -202,3 +202,10 @@ def test_a_graph_notices_what_a_call_overwrites(rd):
     rd.clip_grad_norm([held], 1.0)
     assert bool(held.any())
     assert rd.adapter_plan(make_ids("none", T, n).cuda(), n, out=kept).offsets.tolist() == [0, 0, 0, T]
+
+
+@pytest.mark.parametrize("count", [1, 100])
+def test_a_kept_norm_keeps_no_workspace(rd, count):
+    ts = [randn(k, 100) for k in range(count)]
+    for norm in (rd.grad_norm(ts), rd.clip_grad_norm(ts, 1.0)):
+        assert norm.shape == () and norm.dtype == torch.float32 and norm.untyped_storage().nbytes() == 4
