@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "adapter_plan.h"
 #include "internal.h"
 #include "lora.cuh"
@@ -163,6 +165,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_adapter_plan(const int* __restr
 }
 
 }  // namespace
+
+// Beside the plan's kernel: whoever has a plan has loaded this module.
+static __device__ unsigned int g_plan_error;
+constexpr int kDevices = 64;
+static std::atomic<unsigned int*> g_words[kDevices];
+
+unsigned int* plan_error_word() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return nullptr;
+  unsigned int* word = g_words[dev].load(std::memory_order_acquire);
+  if (word == nullptr) {
+    void* at = nullptr;
+    if (cudaGetSymbolAddress(&at, g_plan_error) != cudaSuccess) return nullptr;
+    word = static_cast<unsigned int*>(at);
+    g_words[dev].store(word, std::memory_order_release);
+  }
+  return word;
+}
+
+cudaError_t take_plan_device_error(unsigned int* flags) {
+  *flags = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev >= kDevices || g_words[dev].load(std::memory_order_acquire) == nullptr) return e;
+  e = cudaMemcpyFromSymbol(flags, g_plan_error, sizeof(*flags));
+  if (e != cudaSuccess || *flags == 0) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_plan_error, &zero, sizeof(zero));
+}
 
 cudaError_t launch_adapter_plan(const int* ids, int64_t T, int n, int* plan, cudaStream_t s) {
   const int bins = n + 1;

@@ -806,8 +806,6 @@ cudaError_t launch_circ_many_fused(const CircMany& a, int p, int dtype, cudaStre
   return many_fused_t<bf16_t>(a, a.g, a.out, p, s, sink);
 }
 
-cudaError_t take_many_fused_plan_error(unsigned int* flags) { return take_error_word(flags); }
-
 cudaError_t launch_circ_bwd_fused(const void* g, const void* x, const float* chat, void* grad_x, float* grad_c,
                                   int64_t B, int D, int p, int dtype, cudaStream_t s, GcSink* sink) {
   const int q = D / p;

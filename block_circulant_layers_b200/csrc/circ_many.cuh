@@ -246,10 +246,9 @@ cudaError_t circ_many_p(int op, const CircMany& a, int dtype, cudaStream_t s, Gc
   return launch_many_gc_p<P, bf16_t>(a, s, sink);
 }
 
-#define RDFFT_CIRC_MANY_INSTANCE(PP)                                                                      \
-  cudaError_t circ_many_##PP(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink) {        \
-    return circ_many_p<PP>(op, a, dtype, s, sink);                                                        \
-  }                                                                                                       \
-  cudaError_t take_circ_many_error_##PP(unsigned int* flags) { return take_error_word(flags); }
+#define RDFFT_CIRC_MANY_INSTANCE(PP)                                                               \
+  cudaError_t circ_many_##PP(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink) { \
+    return circ_many_p<PP>(op, a, dtype, s, sink);                                                 \
+  }
 
 }  // namespace rdfft

@@ -109,8 +109,10 @@ cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, cons
                               float* grad_a, float* grad_b, bool after_rows, const int* plan, int64_t T, int K, int N,
                               int r, int n, int dtype, cudaStream_t s);
 
-// Reads and clears the error words of the kernels that take a plan (bit 0: a plan of other
-// sizes was given).
+// The word of the current device in which the kernels that take a plan record that it was made
+// for other sizes (nullptr if CUDA does not give it), and the call that reads and clears it (bit 0;
+// no CUDA call while no such kernel has been launched on the device).
+unsigned int* plan_error_word();
 cudaError_t take_plan_device_error(unsigned int* flags);
 
 // Global norm and clipping of many tensors (grad_norm, clip_grad_norm in rdfft.h). `ws` holds

@@ -20,6 +20,7 @@ struct PlanView {
   const int* order;
   const int* group;
   const int2* tiles;
+  unsigned int* error;     // plan_error_word()
   int list;
   int T, n;
 };
@@ -32,28 +33,19 @@ inline PlanView plan_view(const int* plan, int64_t T, int n, int list) {
   v.order = plan + l.order;
   v.group = plan + l.group;
   v.tiles = reinterpret_cast<const int2*>(plan + l.tiles[list]);
+  v.error = plan_error_word();
   v.list = list;
   v.T = (int)T;
   v.n = n;
   return v;
 }
 
-// Set by a kernel that was given a plan of other sizes; that kernel then writes nothing.
-// One word per translation unit, read and cleared by rdfft_take_device_error.
-static __device__ unsigned int g_plan_error;
-
-// Uniform over the grid.
+// False, and recorded for rdfft_take_device_error, when the plan was made for other sizes; the
+// kernel then writes nothing. Uniform over the grid.
 __device__ __forceinline__ bool plan_matches(const PlanView& v) {
   if (__ldg(v.header) == v.T && __ldg(v.header + 1) == v.n) return true;
-  if (threadIdx.x == 0) atomicOr(&g_plan_error, 1u);
+  if (threadIdx.x == 0 && v.error != nullptr) atomicOr(v.error, 1u);
   return false;
-}
-
-static cudaError_t take_error_word(unsigned int* flags) {
-  cudaError_t e = cudaMemcpyFromSymbol(flags, g_plan_error, sizeof(*flags));
-  if (e != cudaSuccess || *flags == 0) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(g_plan_error, &zero, sizeof(zero));
 }
 
 // One direction of a low-rank adapter: rows of `in` (T x K) through w1 and w2 to rows of

@@ -890,6 +890,4 @@ cudaError_t lora_wgrad_bf16(const LoraWgrad<bf16_t>& a, cudaStream_t s) {
   return run_wgrad<128>(a, s);
 }
 
-cudaError_t take_lora_bf16_error(unsigned int* flags) { return take_error_word(flags); }
-
 }  // namespace rdfft

@@ -583,6 +583,4 @@ cudaError_t lora_wgrad_f32(const LoraWgrad<float>& a, cudaStream_t s) {
   return run_wgrad<128>(a, s);
 }
 
-cudaError_t take_lora_f32_error(unsigned int* flags) { return take_error_word(flags); }
-
 }  // namespace rdfft

@@ -1,5 +1,4 @@
-// Many-adapter operators: dispatch on the block size or the dtype, and the error words of
-// their translation units.
+// Many-adapter operators: dispatch on the block size or the dtype.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -8,9 +7,8 @@
 namespace rdfft {
 
 #define RDFFT_MANY_P(X) X(64) X(128) X(256) X(512) X(1024) X(2048) X(4096)
-#define RDFFT_MANY_DECL(PP)                                                                      \
-  cudaError_t circ_many_##PP(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink); \
-  cudaError_t take_circ_many_error_##PP(unsigned int* flags);
+#define RDFFT_MANY_DECL(PP) \
+  cudaError_t circ_many_##PP(int op, const CircMany& a, int dtype, cudaStream_t s, GcSink* sink);
 RDFFT_MANY_P(RDFFT_MANY_DECL)
 
 cudaError_t launch_circ_many(int op, const CircMany& a, int p, int dtype, cudaStream_t s, GcSink* sink) {
@@ -95,9 +93,6 @@ cudaError_t lora_rows_bf16(const LoraRows<bf16_t>& a, bool bwd, const int* plan,
 cudaError_t lora_rows_f32(const LoraRows<float>& a, bool bwd, const int* plan, int64_t T, int n, cudaStream_t s);
 cudaError_t lora_wgrad_bf16(const LoraWgrad<bf16_t>& a, cudaStream_t s);
 cudaError_t lora_wgrad_f32(const LoraWgrad<float>& a, cudaStream_t s);
-cudaError_t take_many_fused_plan_error(unsigned int* flags);
-cudaError_t take_lora_bf16_error(unsigned int* flags);
-cudaError_t take_lora_f32_error(unsigned int* flags);
 
 template <typename T>
 static LoraRows<T> rows_args(const void* in, const void* w1, const void* w2, const float* scale, const void* base,
@@ -143,24 +138,6 @@ cudaError_t launch_lora_wgrad(const void* g, const void* x, const float* u, cons
   if (dtype == 0)
     return lora_wgrad_f32(wgrad_args<float>(g, x, u, v, scale, grad_a, grad_b, after_rows, plan, T, K, N, r, n), s);
   return lora_wgrad_bf16(wgrad_args<bf16_t>(g, x, u, v, scale, grad_a, grad_b, after_rows, plan, T, K, N, r, n), s);
-}
-
-cudaError_t take_plan_device_error(unsigned int* flags) {
-  *flags = 0;
-  cudaError_t (*const words[])(unsigned int*) = {
-      take_error_word,
-      take_many_fused_plan_error,
-      take_lora_bf16_error,
-      take_lora_f32_error,
-#define RDFFT_MANY_WORD(PP) take_circ_many_error_##PP,
-      RDFFT_MANY_P(RDFFT_MANY_WORD)};
-  for (auto take : words) {
-    unsigned int f = 0;
-    const cudaError_t e = take(&f);
-    if (e != cudaSuccess) return e;
-    *flags |= f;
-  }
-  return cudaSuccess;
 }
 
 }  // namespace rdfft

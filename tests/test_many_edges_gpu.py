@@ -209,3 +209,61 @@ def test_a_kept_norm_keeps_no_workspace(rd, count):
     ts = [randn(k, 100) for k in range(count)]
     for norm in (rd.grad_norm(ts), rd.clip_grad_norm(ts, 1.0)):
         assert norm.shape == () and norm.dtype == torch.float32 and norm.untyped_storage().nbytes() == 4
+
+
+def run_alone(code):
+    """Runs a program of its own and returns the last line it prints."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    return r.stdout.strip().splitlines()[-1]
+
+
+def test_reading_the_device_error_costs_one_copy_per_word(rd):
+    """Every copy waits for the device: three words of the transforms' kernels, and one of all kernels
+    that take a plan, read only once one of them has been launched."""
+    code = """
+import torch, block_circulant_layers_b200 as rd
+from torch.profiler import profile, ProfilerActivity
+def copies():
+    with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as p:
+        assert rd.take_device_error() == 0
+    return sum("Memcpy DtoH" in e.name for e in p.events())
+x = torch.randn(4, 128, device="cuda")
+rd.rdfft_fwd(x, 64)
+copies()
+before = copies()
+plan = rd.adapter_plan(torch.zeros(4, dtype=torch.int32, device="cuda"), 1)
+rd.circ_fwd_many(x, torch.randn(1, 2, 2, 64, device="cuda"), 64, plan)
+rd.lora_fwd(x, torch.randn(1, 8, 128, device="cuda"), torch.randn(1, 64, 8, device="cuda"), plan)
+print(before, copies())
+"""
+    assert run_alone(code) == "3 4"
+
+
+def test_a_programs_first_calls_are_captured(rd):
+    """Nothing of the library is loaded before the capture begins; the replay gives an eager call's bits."""
+    code = """
+import torch, block_circulant_layers_b200 as rd
+torch.manual_seed(0)
+T, n, K = 40, 2, 128
+ids = torch.randint(-1, n, (T,), dtype=torch.int32, device="cuda")
+x, a, b = torch.randn(T, K, device="cuda"), torch.randn(n, 8, K, device="cuda"), torch.randn(n, K, 8, device="cuda")
+c, u = torch.randn(n, 2, 2, 64, device="cuda"), torch.empty(T, 8, device="cuda")
+def step():
+    plan = rd.adapter_plan(ids, n)
+    y = rd.lora_fwd(x, a, b, plan, u=u)
+    grads = [*rd.lora_bwd(y, x, a, b, plan, u), rd.circ_fwd_many(x, c, 64, plan), *rd.circ_bwd_many(y, x, c, 64, plan)]
+    return [y, *grads, rd.grad_norm(grads)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+print(all(torch.equal(p, q) for p, q in zip(got, want)), rd.take_device_error())
+"""
+    assert run_alone(code) == "True 0"
