@@ -31,6 +31,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 LIB = os.path.join(PKG, "librdfft.so")
 NATIVE = os.path.join(PKG, "_native.so")
+NATIVE_ABI = os.path.join(PKG, "_native.abi")      # what _native.so was built for
 EMU = os.path.join(PKG, "librdfft_hostemu.so")
 
 CU_SOURCES = ["rdfft_api.cu", "rdfft_kernels.cu", "rdfft2d_kernels.cu", "convert_kernels.cu", "circ_launch.cu",
@@ -114,9 +115,24 @@ def build_lib(force=False, verbose=False, ptxas_info=False) -> str:
     return LIB
 
 
+def native_abi() -> str:
+    """What _native.so is tied to beside its sources: the C++ ABI of this torch and of this Python."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, cxx11 {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _native_current() -> bool:
+    if not _up_to_date(NATIVE) or not os.path.exists(NATIVE_ABI):
+        return False
+    with open(NATIVE_ABI) as f:
+        return f.read() == native_abi()
+
+
 def build_native(force=False, verbose=False) -> str:
-    build_lib(force=force, verbose=verbose)
-    if not force and _up_to_date(NATIVE):
+    build_lib(verbose=verbose)
+    if not force and _native_current():
         return NATIVE
     import sysconfig
 
@@ -133,6 +149,8 @@ def build_native(force=False, verbose=False) -> str:
          + [os.path.join(CSRC, "native_binding.cpp"), "-o", tmp, "-L", PKG, "-l:librdfft.so", "-L", torch_lib,
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, NATIVE)
+    with open(NATIVE_ABI, "w") as f:
+        f.write(native_abi())
     return NATIVE
 
 
@@ -150,7 +168,7 @@ def build_emulator(force=False, verbose=False) -> str:
 
 def build(force=False, verbose=False, emulator=True) -> None:
     build_lib(force=force, verbose=verbose)
-    build_native(verbose=verbose)
+    build_native(force=force, verbose=verbose)
     if emulator:
         build_emulator(force=force, verbose=verbose)
 
@@ -163,7 +181,7 @@ def main(argv=None) -> int:
     ap.add_argument("-v", "--verbose", action="store_true")
     a = ap.parse_args(argv)
     build_lib(force=a.force or a.ptxas_info, verbose=a.verbose, ptxas_info=a.ptxas_info)
-    build_native(verbose=a.verbose)
+    build_native(force=a.force, verbose=a.verbose)
     if not a.no_emulator:
         build_emulator(force=a.force, verbose=a.verbose)
     print(LIB)
