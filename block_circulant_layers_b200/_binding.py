@@ -20,11 +20,22 @@ if not os.path.exists(lib_path):
 
 lib = ctypes.CDLL(lib_path)
 
+
+class _NoNative:
+    """Stands for _native where it does not load: its calls say why, the others work without it."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the _native module next to {lib_path} is missing or does not load ({self._why}): build "
+                          "it with `python -m block_circulant_layers_b200.build`") from self._why
+
+
 try:
     from . import _native  # noqa: E402  (linked against librdfft.so beside it)
 except ImportError as e:
-    raise ImportError(f"the _native module next to {lib_path} is missing or does not load: build it with "
-                      "`python -m block_circulant_layers_b200.build`") from e
+    _native = _NoNative(e)
 
 _i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 lib.rdfft_fwd.argtypes = [_vp, _i64, _int, _int, _vp]

@@ -41,3 +41,29 @@ def test_the_scale_follows_the_device(many):
     assert bank.scale.device.type == "meta" and bank.scale.dtype == torch.float32
     bank = torch.nn.Sequential(many.LowRankAdapters(2, 64, 72, 24, alpha=8.0)).to(torch.bfloat16)
     assert bank[0].scale.dtype == torch.float32 and float(bank[0].scale[0]) == float(torch.tensor(8.0 / 24.0))
+
+
+def test_the_older_calls_work_without_the_cpp_binding(many):
+    """A _native module that does not load (torch has changed, say) leaves the ctypes calls usable; the
+    calls that need it say what to do."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    code = """
+import sys
+sys.modules["block_circulant_layers_b200._native"] = None     # importing it raises ImportError
+import torch, block_circulant_layers_b200 as rd
+assert rd.circ_bwd_workspace_size(64, 1024, 128, torch.float32) > 0
+rd.BlockCirculantLinear(128, 64)
+rd.LowRankAdapters(2, 64, 64, 8)
+for call in (lambda: rd.adapter_plan(torch.zeros(4, dtype=torch.int32), 2), lambda: rd.grad_norm([torch.zeros(4)])):
+    try:
+        call()
+    except ImportError as e:
+        assert "block_circulant_layers_b200.build" in str(e), e
+    else:
+        raise AssertionError("no error")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
