@@ -343,7 +343,9 @@ int lora_fwd(const void* x, const void* a, const void* b, const float* scale, co
  * What a skipped gradient alone needs may be NULL: x for grad_a, u for grad_b, a for grad_x.
  * No output may overlap any other argument. Sums over tokens are fp32 as in lora_fwd and run in a
  * fixed order: the gradients are the same on every run. v is rounded to fp32 before grad_a's sum
- * (in bf16, u and v enter it as three bf16 each, 24 mantissa bits).
+ * (in bf16, u and v enter it as three bf16 each, 24 mantissa bits). An infinity or NaN of a token
+ * stays in its row of grad_x and in its adapter's grad_a and grad_b, where a bf16 call may give NaN
+ * instead of infinite.
  */
 int lora_bwd(const void* g, const void* x, const void* a, const void* b, const float* scale, const float* u, float* v,
              void* grad_x, float* grad_a, float* grad_b, const int32_t* plan, int64_t T, int K, int N, int r, int n,

@@ -267,3 +267,156 @@ want = step()
 print(all(torch.equal(p, q) for p, q in zip(got, want)), rd.take_device_error())
 """
     assert run_alone(code) == "True 0"
+
+
+# ----------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,r,kind", [(40, 24, "mixed"), (1500, 24, "runs"), (1500, 64, "runs"), (1030, 128, "mixed")])
+def test_values_that_are_not_finite_stay_where_they_belong(rd, T, r, kind, dtype):
+    """An infinity or NaN in one token's x, g or base reaches that token's rows and its adapter's weight
+    gradients only, with the tiles of 16 and of 64 tokens and whatever shares a tile with it; in a
+    token without an adapter it reaches nothing but a copied base row. All else has the same bits."""
+    n, K, N, dt = 5, 136, 200, DT[dtype]
+    ids = make_ids(kind, T, n, seed=3)
+    x, g, base = randn(1, T, K, dtype=dt), randn(2, T, N, dtype=dt), randn(3, T, N, dtype=dt)
+    a, b = randn(4, n, r, K, std=0.1, dtype=dt), randn(5, n, N, r, std=0.2, dtype=dt)
+    plan = rd.adapter_plan(ids.cuda(), n)
+    u = torch.empty(T, r, device="cuda")
+
+    def calls():
+        y = rd.lora_fwd(x, a, b, plan, base=base, u=u)
+        return [y, u.clone(), *rd.lora_bwd(g, x, a, b, plan, u)]
+
+    clean = calls()
+    assert all(bool(torch.isfinite(t).all()) for t in clean)
+    bad = int((ids == 2).nonzero()[1])
+    none = int((ids < 0).nonzero()[0])
+    others = torch.ones(T, dtype=torch.bool)
+    others[bad] = False
+    for value in (float("inf"), float("nan")):
+        for t in (x, g):
+            keep = t.clone()
+            t[bad, 5] = value
+            t[none, 7] = value                                # a token without an adapter: never read
+            y, uu, gx, ga, gb = calls()
+            t.copy_(keep)
+            for got, want in ((y, clean[0]), (uu, clean[1]), (gx, clean[2])):
+                assert torch.equal(got[others.cuda()], want[others.cuda()])
+            for got, want in ((ga, clean[3]), (gb, clean[4])):
+                rest = [k for k in range(n) if k != 2]
+                assert torch.equal(got[rest], want[rest])
+            if t is x:
+                assert not bool(torch.isfinite(y[bad]).any()) and not bool(torch.isfinite(uu[bad]).any())
+                assert not bool(torch.isfinite(gb[2]).any())                # through u
+                assert not bool(torch.isfinite(ga[2, :, 5]).any())          # v x, column 5 alone
+                assert torch.equal(ga[2, :, :5], clean[3][2, :, :5]) and torch.equal(gx, clean[2])
+            else:
+                assert not bool(torch.isfinite(gx[bad]).any())
+                assert not bool(torch.isfinite(ga[2]).any())                # through v
+                assert not bool(torch.isfinite(gb[2, 5]).any())             # g u, row 5 alone
+                assert torch.equal(gb[2, :5], clean[4][2, :5]) and torch.equal(y, clean[0])
+    keep = base.clone()
+    base[none, 7] = base[bad, 9] = float("nan")
+    y, uu, gx, ga, gb = calls()
+    base.copy_(keep)
+    wrong = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    wrong[none, 7] = wrong[bad, 9] = True
+    assert bool(y[wrong].isnan().all()) and torch.equal(y[~wrong], clean[0][~wrong])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,p", [(40, 512, 64), (600, 4096, 512), (90, 1024, 1024), (300, 4096, 128), (50, 640, 128)])
+def test_a_circulant_value_that_is_not_finite_stays_where_it_belongs(rd, T, D, p, dtype):
+    """The same for the block-circulant adapters."""
+    n, q, dt = 4, D // p, DT[dtype]
+    ids = make_ids("runs", T, n, seed=3)
+    ids[::7], ids[1], ids[2] = -1, 2, 1
+    x, g, base = randn(1, T, D, dtype=dt), randn(2, T, D, dtype=dt), randn(3, T, D, dtype=dt)
+    c_hat = rd.rdfft_fwd(randn(4, n, q, q, p, std=D ** -0.5), p)
+    plan = rd.adapter_plan(ids.cuda(), n)
+
+    def calls():
+        return [rd.circ_fwd_many(x, c_hat, p, plan, base=base), *rd.circ_bwd_many(g, x, c_hat, p, plan)]
+
+    clean = calls()
+    others = torch.ones(T, dtype=torch.bool)
+    others[1] = False
+    others = others.cuda()
+    for value in (float("inf"), float("nan")):
+        for t in (x, g):
+            keep = t.clone()
+            t[1, 5] = t[0, 3] = value                         # token 0 has no adapter
+            y, gx, gc = calls()
+            t.copy_(keep)
+            assert torch.equal(y[others], clean[0][others]) and torch.equal(gx[others], clean[1][others])
+            rest = [k for k in range(n) if k != 2]
+            assert torch.equal(gc[rest], clean[2][rest]) and bool((~torch.isfinite(gc[2])).any())
+            assert bool((~torch.isfinite(y[1] if t is x else gx[1])).any())
+            assert torch.equal(gx if t is x else y, clean[1] if t is x else clean[0])
+
+
+# ------------------------------------------------------------------- offsets past 32 bits
+# The tokens past element 2^31 are 16 times as large as the others, so that the sums are theirs.
+@pytest.mark.parametrize("wide", ["x", "g"])
+def test_lora_weight_gradients_past_32_bits(rd, wide):
+    T, W, r, n = 66000, 32768, 8, 2
+    first = 2 ** 31 // W
+    assert first < T
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    big = torch.empty(T, W, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    big[first:] *= 16
+    small = randn(2, T, 8, dtype=torch.bfloat16)
+    K, N = (W, 8) if wide == "x" else (8, W)
+    x, g = (big, small) if wide == "x" else (small, big)
+    a, b = randn(3, n, r, K, std=K ** -0.5, dtype=x.dtype), randn(4, n, N, r, std=0.3, dtype=x.dtype)
+    ids = ((torch.arange(T) % 3 - 1).int()).cuda()
+    plan = rd.adapter_plan(ids, n)
+    u = torch.empty(T, r, device="cuda")
+    rd.lora_fwd(x, a, b, plan, u=u)
+    _, ga, gb = rd.lora_bwd(g, x, a, b, plan, u, need_grad_x=False)
+    from many_util import assert_within, sum_bound
+    for k in range(n):
+        rows = (ids == k).nonzero().flatten()
+        gd = torch.cat([t.double() @ b[k].double() for t in g[rows].split(2048)])        # v
+        gm = torch.cat([t.double().abs() @ b[k].double().abs() for t in g[rows].split(2048)])
+        ud = u[rows].double()
+        for at in (0, W // 2 + 24, W - 64):
+            cols = slice(at, at + 64)
+            xs, gs = x[rows, cols if wide == "x" else slice(None)], g[rows, cols if wide == "g" else slice(None)]
+            ref, mag = gd.t() @ xs.double(), gm.t() @ xs.double().abs()
+            got = ga[k][:, cols] if wide == "x" else ga[k]
+            bound = sum_bound(N, 1, x.dtype) + sum_bound(3 * rows.numel(), 1, x.dtype)
+            assert_within(got, ref.cpu(), (bound * mag).cpu(), "grad_a")
+            ref, mag = gs.double().t() @ ud, gs.double().abs().t() @ ud.abs()
+            got = gb[k][cols] if wide == "g" else gb[k]
+            assert_within(got, ref.cpu(), (sum_bound(3 * rows.numel(), 1, x.dtype) * mag).cpu(), "grad_b")
+
+
+@pytest.mark.parametrize("alone", [False, True])
+def test_circulant_weight_gradients_past_32_bits(rd, alone):
+    T, D, p, n = 530000, 4096, 512, 2
+    first = 2 ** 31 // D
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    g = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    x[first:] *= 16
+    g[first:] *= 16
+    ids = ((torch.arange(T) % 3 - 1).int()).cuda()
+    plan = rd.adapter_plan(ids, n)
+    c_hat = rd.rdfft_fwd(randn(2, n, 8, 8, p, std=D ** -0.5), p)
+    gc = rd.circ_bwd_many(g, x, c_hat, p, plan, need_grad_x=not alone)[1]
+    for k in range(n):
+        rows = (ids == k).nonzero().flatten()
+        for i, j in ((0, 0), (3, 6), (7, 7)):
+            s = torch.zeros(p // 2 + 1, dtype=torch.complex128, device="cuda")
+            mag = 0.0
+            for part in rows.split(1 << 14):
+                gi, xj = (t[part, c * p:(c + 1) * p].double() for t, c in ((g, i), (x, j)))
+                s += (torch.fft.rfft(gi) * torch.fft.rfft(xj).conj()).sum(0)
+                mag += float((gi.norm(dim=1) * xj.norm(dim=1)).sum())       # a term of a lag is at most this
+            ref = torch.fft.irfft(s, n=p)
+            # fp32 sums over a slice's tokens (148 slices), then over the slices, with the layer's own
+            # error (1e-5 of the largest value) for the transforms
+            bound = 4 * (T / 148 + 148) ** 0.5 * 2.0 ** -24 * mag + 1e-5 * float(ref.abs().max())
+            assert float((gc[k, i, j].double() - ref).abs().max()) <= bound
+            assert float(ref.norm()) / p ** 0.5 > 10 * bound                 # a lost part would show
