@@ -507,6 +507,12 @@ int grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes
               void* workspace, size_t workspace_bytes, rdfft_stream_t stream) {
   const int rc = norm_args(grads, numels, dtypes, count, norm, workspace, workspace_bytes);
   if (rc != RDFFT_OK) return rc;
+  const size_t ws = sizeof(double) * (size_t)rdfft::grad_norm_ws_doubles(count);
+  if (overlap(norm, sizeof(float), workspace, ws)) return RDFFT_EOVERLAP;
+  for (int i = 0; i < count; ++i) {
+    const size_t bytes = (dtypes[i] == RDFFT_F32 ? 4 : 2) * (size_t)numels[i];
+    if (overlap(grads[i], bytes, norm, sizeof(float)) || overlap(grads[i], bytes, workspace, ws)) return RDFFT_EOVERLAP;
+  }
   return finish(rdfft::launch_grad_norm(grads, nullptr, numels, dtypes, count, 0.0f, norm,
                                         static_cast<double*>(workspace), reinterpret_cast<cudaStream_t>(stream)));
 }

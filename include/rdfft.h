@@ -401,7 +401,8 @@ int grad_norm_workspace_size(int count, size_t* bytes);
  *            The tensors are dense and need only their element's alignment.
  *   norm   : one fp32 on the device, written (0 for no elements).
  *   workspace : grad_norm_workspace_size bytes, 8-byte aligned; overwritten. Calls that share
- *            it must be ordered on one stream.
+ *            it must be ordered on one stream. Neither it nor the norm may overlap anything else
+ *            (RDFFT_EOVERLAP).
  * Sums are double (of fp32 sums of 8 squares where those neither overflow nor underflow) and
  * in a fixed order. A NaN or infinite element makes the norm NaN or infinite.
  */
