@@ -5,6 +5,7 @@
 // 9 us on the device, clip_grad_norm of 64 tensors 121 us against 12 us). Each function
 // returns the C ABI's code first; _binding.py turns it into an RdfftError.
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <pybind11/pybind11.h>
@@ -277,15 +278,16 @@ py::tuple norm_(const py::list& ts, bool clip, double max_norm, const std::optio
   const int rc = grad_norm_workspace_size(count, &need);
   if (rc != RDFFT_OK) return py::make_tuple(rc, py::none());
   const c10::cuda::OptionalCUDAGuard guard(in.first.device());
-  // memory of its own for the norm: a caller may keep it long after the workspace
-  const Tensor buf = at::empty({(int64_t)need}, in.first.options().dtype(at::kByte));
+  // memory of its own for the norm: a caller may keep it long after the workspace, which needs no
+  // tensor around it (0.5 us of the 11 that 64 tensors take)
+  const c10::DataPtr ws = c10::cuda::CUDACachingAllocator::get()->allocate(need);
   const Tensor norm = at::empty({}, in.first.options().dtype(at::kFloat));
   float* const n = norm.mutable_data_ptr<float>();
   const void* const* grads = const_cast<const void* const*>(in.ptrs.data());
   const int code =
       clip ? clip_grad_norm(grads, out ? o.ptrs.data() : in.ptrs.data(), in.numels.data(), in.codes.data(), count,
-                            (float)max_norm, n, buf.data_ptr(), need, stream_of(buf))
-           : grad_norm(grads, in.numels.data(), in.codes.data(), count, n, buf.data_ptr(), need, stream_of(buf));
+                            (float)max_norm, n, ws.get(), need, stream_of(norm))
+           : grad_norm(grads, in.numels.data(), in.codes.data(), count, n, ws.get(), need, stream_of(norm));
   if (clip)
     for (py::handle t : out ? *out : ts) written(code, THPVariable_Unpack(t.ptr()));
   return py::make_tuple(code, norm);
