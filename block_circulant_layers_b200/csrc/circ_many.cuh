@@ -51,7 +51,7 @@ k_circ_many_x(const T* __restrict__ in, const float* __restrict__ chat, const T*
     const int2 te = __ldg(plan.tiles + tile);               // within the list's capacity
     if (tile >= __ldg(plan.header + 2 + plan.list)) return;
     pos = te.x + sub * TT, ad = te.y;
-    m = min(__ldg(plan.offsets + ad + 1) - pos, TT);
+    m = min(__ldg(plan.offsets() + ad + 1) - pos, TT);
     if (m <= 0) return;
   }
   const int o0 = blockIdx.y * QI, D = q * P;
@@ -85,7 +85,7 @@ struct SliceWalk {
   int ad;
   bool whole;                                               // all of them
   __device__ __forceinline__ explicit SliceWalk(const PlanView& v) {
-    const int64_t tokens = __ldg(v.offsets + v.n);
+    const int64_t tokens = __ldg(v.offsets() + v.n);
     const int64_t slices = min((int64_t)gridDim.x, tokens);
     pos = hi = 0;
     if (blockIdx.x < slices) {
@@ -100,9 +100,9 @@ struct SliceWalk {
     if (pos >= hi) return false;
     ad = __ldg(v.group + pos);
     beg = pos;
-    const int64_t all = __ldg(v.offsets + ad + 1);
+    const int64_t all = __ldg(v.offsets() + ad + 1);
     end = min(all, hi);
-    whole = end == all && beg == __ldg(v.offsets + ad);
+    whole = end == all && beg == __ldg(v.offsets() + ad);
     pos = end;
     return true;
   }
@@ -117,7 +117,7 @@ struct SliceWalk {
 // grad_x of the tokens without an adapter: zeros in blocks [j0, j0 + QJ), shared by the slices.
 template <int P, typename T>
 __device__ __forceinline__ void zero_unplanned(T* grad_x, const PlanView& v, int q, int j0, int QJ) {
-  const int beg = __ldg(v.offsets + v.n), end = __ldg(v.offsets + v.n + 1), w = QJ * P;
+  const int beg = __ldg(v.offsets() + v.n), end = __ldg(v.offsets() + v.n + 1), w = QJ * P;
   constexpr int V = 16 / (int)sizeof(T);
   for (int t = beg + blockIdx.x; t < end; t += gridDim.x) {
     T* const row = grad_x + (int64_t)__ldg(v.order + t) * q * P + (int64_t)j0 * P;

@@ -16,20 +16,20 @@ namespace rdfft {
 // The parts of a plan that one kernel reads, and the sizes it must have been made for.
 struct PlanView {
   const int* header;
-  const int* offsets;
   const int* order;
   const int* group;
   const int2* tiles;
   unsigned int* error;     // plan_error_word()
   int list;
   int T, n;
+  // Behind the header in every plan, so not a field: with one more, the 64-token rows kernels spill.
+  __device__ __forceinline__ const int* offsets() const { return header + kPlanHeader; }
 };
 
 inline PlanView plan_view(const int* plan, int64_t T, int n, int list) {
   const PlanLayout l = plan_layout(T, n);
   PlanView v;
   v.header = plan;
-  v.offsets = plan + l.offsets;
   v.order = plan + l.order;
   v.group = plan + l.group;
   v.tiles = reinterpret_cast<const int2*>(plan + l.tiles[list]);
@@ -96,8 +96,8 @@ constexpr int kWindow = 254;
 struct TileShare {
   int lo, hi, all, end;                     // of `all` tiles with an adapter, whose positions end at `end`
   __device__ __forceinline__ TileShare(const PlanView& v, unsigned rank, unsigned C) {
-    end = __ldg(v.offsets + v.n);
-    const int none = __ldg(v.offsets + v.n + 1) - end;
+    end = __ldg(v.offsets() + v.n);
+    const int none = __ldg(v.offsets() + v.n + 1) - end;
     all = __ldg(v.header + 2 + v.list) - (none + 63) / 64;
     lo = (int)((int64_t)all * rank / C);
     hi = (int)((int64_t)all * (rank + 1) / C);

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) k_lora_rows16(LoraR
   const int2 te = __ldg(a.plan.tiles + tile);                  // within the list's capacity
   if (tile >= __ldg(a.plan.header + 2 + a.plan.list)) return;  // the whole cluster leaves
   const int pos0 = te.x, ad = te.y;
-  const int m = min(__ldg(a.plan.offsets + ad + 1) - pos0, M);
+  const int m = min(__ldg(a.plan.offsets() + ad + 1) - pos0, M);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
   const int K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
   const int2 te = __ldg(a.plan.tiles + tile);                  // within the list's capacity
   if (tile >= __ldg(a.plan.header + 2 + a.plan.list)) return;  // the whole cluster leaves
   const int pos0 = te.x, ad = te.y;
-  const int m = min(__ldg(a.plan.offsets + ad + 1) - pos0, M);
+  const int m = min(__ldg(a.plan.offsets() + ad + 1) - pos0, M);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, q = lane % 4;
   const int K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
@@ -834,7 +834,7 @@ k_lora_wgrad(LoraWgrad<bf16_t> a, int blocks_b) {
   // adapters without tokens, shared by the cluster: zeros, whatever their scale holds
   clear();
   for (int ad = rank; ad < a.plan.n; ad += C)
-    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad, 1.0f);
+    if (__ldg(a.plan.offsets() + ad) == __ldg(a.plan.offsets() + ad + 1)) write(ad, 1.0f);
   if (C > 1) cluster_wait();                                   // the others are done with this CTA's memory
   if (early) griddep_wait();
 }

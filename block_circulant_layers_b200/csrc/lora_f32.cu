@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
   const int2 te = __ldg(a.plan.tiles + tile);               // within the list's capacity
   if (tile >= __ldg(a.plan.header + 2 + a.plan.list)) return;   // the whole cluster leaves
   const int pos0 = te.x, ad = te.y;
-  const int m = min(__ldg(a.plan.offsets + ad + 1) - pos0, M);
+  const int m = min(__ldg(a.plan.offsets() + ad + 1) - pos0, M);
   const int tid = threadIdx.x, K = a.K, N = a.N, r = a.r;
   const bool adapted = ad < a.plan.n;
 
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, WgradF32<R>::kPerSM) k_lora_wgrad_f3
 #pragma unroll
   for (int e = 0; e < NA; ++e) sum[e] = 0.0f;
   for (int ad = rank; ad < a.plan.n; ad += C)               // adapters without tokens: zeros, whatever their scale holds
-    if (__ldg(a.plan.offsets + ad) == __ldg(a.plan.offsets + ad + 1)) write(ad, 1.0f);
+    if (__ldg(a.plan.offsets() + ad) == __ldg(a.plan.offsets() + ad + 1)) write(ad, 1.0f);
   if (C > 1) cluster_wait();                                // the others are done with this CTA's memory
   if (early) griddep_wait();
 }

@@ -34,9 +34,9 @@ __global__ void __launch_bounds__(kSumThreads) k_sum_slots(const float4* __restr
   if (!plan_matches(plan)) return;
   const int ad = blockIdx.y, el = threadIdx.x % EPB, r = threadIdx.x / EPB;
   const int64_t e = (int64_t)blockIdx.x * EPB + el;
-  const int64_t tokens = __ldg(plan.offsets + plan.n);
+  const int64_t tokens = __ldg(plan.offsets() + plan.n);
   slices = (int)min((int64_t)slices, tokens);
-  const int beg = __ldg(plan.offsets + ad), end = __ldg(plan.offsets + ad + 1);
+  const int beg = __ldg(plan.offsets() + ad), end = __ldg(plan.offsets() + ad + 1);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // the slice of a position: the last s with tokens s / slices <= position
   const int first = beg < end ? (int)(((int64_t)(beg + 1) * slices - 1) / tokens) : 0;
