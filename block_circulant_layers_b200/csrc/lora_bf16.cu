@@ -629,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_rows64(LoraRows<bf16_t> a)
 // steps ahead, its token numbers two or three steps before that.
 // mid is fp32; it enters the product as three bf16 that sum to it in all but its last bits
 // (24 mantissa bits), since the gradients are fp32.
-// K = N = 4096, r = 16, 4096 tokens: 21.4 us for the 67 MB of x and g (about 8 us of start and
-// end, the tiles between them near the copy rate), r = 64 54 us. A CTA per adapter and column group,
-// whatever the group's size, took 41 us on uneven groups (r = 16).
+// K = N = 4096, 4096 tokens of 8 adapters, from cold L2: r = 16 26 us for the 67 MB of x and g (10 at the
+// copy rate; start and end take about 8), r = 64 78 us, r = 128 163 us. A CTA per adapter and column
+// group, whatever the group's size, took 41 us on uneven groups where this takes 26 (r = 16).
 template <int R>
 struct Wgrad {
   static constexpr int kCols = R <= 32 ? 128 : 64, kTok = 64, kOrders = 8;

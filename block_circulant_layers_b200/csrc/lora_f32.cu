@@ -5,7 +5,7 @@
 // output columns, pass through one ring of cp.async stages; operands keep their own row order, padded
 // by 16 bytes a row, and are read 4 contraction indices at a time; sums are kept on packed fp32
 // pairs. Shared-memory reads and their latency bound it: K = N = 2048, r = 16, 4096 tokens 39.2 us
-// forward (101 MB: 15 us); K = N = 4096, r = 64 157 us (27 TFLOP/s).
+// forward (101 MB: 15 us); K = N = 4096, r = 64 163 us (26 TFLOP/s).
 #include "lora.cuh"
 
 #include "many_policy.h"
@@ -33,8 +33,6 @@ __device__ __forceinline__ void lds(const float* p, float (&v)[N]) {
     }
   }
 }
-
-__device__ __forceinline__ float4 ldg4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 template <int R, int M, bool BWD>
 struct RowsShape {
@@ -315,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows_f32(LoraRows<float> a) {
 // thread has 4 columns x RT values of r, of a share of the tile's tokens while r <= 32 (a
 // smaller register tile would read shared memory as often as it multiplies); the shares are
 // added in order when an adapter is complete.
-// K = N = 4096, 4096 tokens: r = 16 41 us (134 MB: 21 us; without the shares 65), r = 64 90 us.
+// K = N = 4096, 4096 tokens of 8 adapters, from cold L2: r = 16 57 us (134 MB: 21 us), r = 64 143 us.
 template <int R>
 struct WgradF32 {
   static constexpr int kTok = 64, kStages = 2, kOrders = 8;
