@@ -80,8 +80,8 @@ class _CirculantManyFn(torch.autograd.Function):
 
 def low_rank_many(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: _b.AdapterPlan,
                   scale: torch.Tensor | None = None, base: torch.Tensor | None = None) -> torch.Tensor:
-    """y_t = base_t + scale_k b_k (a_k x_t); a (n, r, K) and b (n, N, r) are used in x's dtype.
-    scale (n,) float32 takes no gradient."""
+    """y_t = base_t + scale_k b_k (a_k x_t); a (n, r, K), b (n, N, r) and base are used in x's dtype,
+    which is y's. scale (n,) float32 takes no gradient."""
     if scale is not None and scale.requires_grad:
         raise ValueError("scale takes no gradient")
     return _LowRankFn.apply(x, a, b, plan, scale, base)
@@ -89,7 +89,7 @@ def low_rank_many(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: _b.Ad
 
 def block_circulant_many(x: torch.Tensor, c: torch.Tensor, p: int, plan: _b.AdapterPlan,
                          base: torch.Tensor | None = None) -> torch.Tensor:
-    """y_t = base_t + W(c_k) x_t; c (n, q, q, p) float32."""
+    """y_t = base_t + W(c_k) x_t; c (n, q, q, p) float32, base used in x's dtype, which is y's."""
     return _CirculantManyFn.apply(x, c, p, plan, base)
 
 
